@@ -593,6 +593,159 @@ BATQ_API batq_status batq_linear_no_alloc(const void* X, batq_dtype x_dtype, int
                                           const uint8_t* w_codes, const uint8_t* w_scales, int M,
                                           batq_dtype out_dtype, void* out, int ldo, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Serving operators: what a decode step needs beside the W4A4 linear.  The
+ * method's pages have no counterpart of these calls; the weights, their
+ * formats and the transform are those of the calls above.
+ * ------------------------------------------------------------------------ */
+
+/* 4-bit weight formats of batq_linear_w4a16 (as batq_prepare_weights and batq_prepare_weights_nvfp4 write them). */
+typedef enum { BATQ_W4_MXFP4 = 0, BATQ_W4_NVFP4 = 1 } batq_w4_format;
+
+/*
+ * Linear layer of 1 to 16 tokens with 4-bit weights and activations that are
+ * not quantised (W4A16): for every token s and out-feature m
+ *   out[s][m] = sum_n y[s][n] deq(W')[m][n],   y_s = x_s P (P_i = B_i (x) A),
+ * or y = x when A_host and B_dev are both NULL (weights prepared with an
+ * identity transform, or any 4-bit weights with group scales in these formats).
+ * The weights' bytes are read once (for N up to 16384; beyond, the tokens of a
+ * call go in groups that a launch can hold).
+ *
+ * X: device, S rows of N elements (x_dtype), row stride ldx as batq_quant_act.
+ * A_host, B_dev: as batq_quant_act, or both NULL.
+ * w_codes, w_scales: M rows, MMA scale layout.  w_gs_dev: NVFP4 only, the
+ *    device float that batq_prepare_weights_nvfp4 wrote, or NULL (1).
+ * Accuracy: y is kept to 22 bits relative to its token's largest value (bf16 X
+ * without a transform exactly), products are exact and summed in fp32.
+ * Non-finite x make the token's outputs non-finite (NaN, or an infinity).
+ * Errors: BATQ_ERR_INVALID_ARG (also: only one of A_host and B_dev, w_gs_dev
+ * with MXFP4), BATQ_ERR_SHAPE (S > 16, N % 64 != 0 or N > 131072, M % 16 != 0),
+ * BATQ_ERR_ALIGNMENT, BATQ_ERR_ARCH, BATQ_ERR_CUDA.
+ */
+BATQ_API batq_status batq_linear_w4a16(const void* X, batq_dtype x_dtype, int S, int N, int ldx,
+                                       const float* A_host, const float* B_dev, batq_w4_format w_format,
+                                       const uint8_t* w_codes, const uint8_t* w_scales, const float* w_gs_dev,
+                                       int M, batq_dtype out_dtype, void* out, int ldo, void* stream);
+
+/*
+ * The 8-bit paged cache with a scale per page and kv head.  K and V each hold
+ * num_pages x kv_heads x page_size x head_dim E4M3 codes and num_pages x
+ * kv_heads E8M0 scale bytes; value = code * 2^(byte - 127).  head_dim is 64,
+ * 128 or 256, page_size 16, 32, 64 or 128.  Token t of sequence b lies in page
+ * page_table[b * max_pages + t / page_size] at row t % page_size; a page id
+ * outside [0, num_pages) names no page.  A batch has `batch` sequences;
+ * seq_lens_dev[b] counts the tokens of sequence b in the cache, those that the
+ * call brings among them.  The rows of sequence b are cu[b] .. cu[b + 1] - 1
+ * of the call's T rows; cu == NULL: row b alone (T >= batch).  Rows behind
+ * cu[batch] (padding) belong to no sequence.  A sequence whose range is not
+ * inside [0, T] or is decreasing has no rows.
+ *
+ * (batq_quant_kv_cache writes the other cache format of this library: a scale
+ * per token and 32 elements, with the block transform.)
+ */
+
+/*
+ * Appends new K and V rows.  Row i of a sequence with n new rows is its token
+ * seq_lens[b] - n + i.  A block (a page's rows of one head) has the smallest
+ * scale 2^e, e >= -127, with |x| <= 448 * 2^e for all finite values written to
+ * it since its page's first token was; codes are E4M3(x * 2^-e), rounded to
+ * nearest even.  A token that raises e multiplies the codes already there by
+ * the power of two between, rounding again (exact except for E4M3
+ * subnormals).  A page's first token (row 0) starts the block afresh.  NaN and
+ * infinities are stored as NaN (0x7F) and take no part in the scale.
+ *
+ * K, V: device, T rows of kv_heads * head_dim elements (dtype), row strides
+ * ldk and ldv (16-byte multiples), 16-byte aligned.  Codes 16-byte aligned.
+ * Tokens whose page is not named, or lies behind the page table, are dropped,
+ * and so is a sequence with seq_lens[b] < n.  Rows of a page behind the new
+ * tokens, and pages without new tokens, keep their bytes.  Two sequences of a
+ * call must not write the same page.
+ * Errors: BATQ_ERR_INVALID_ARG, BATQ_ERR_SHAPE, BATQ_ERR_ALIGNMENT,
+ * BATQ_ERR_ARCH, BATQ_ERR_CUDA.
+ */
+BATQ_API batq_status batq_kv8_append(const void* K, const void* V, batq_dtype dtype, int T, int kv_heads,
+                                     int head_dim, int ldk, int ldv, const int* cu_new_dev,
+                                     const int* seq_lens_dev, const int* page_table_dev, int batch, int max_pages,
+                                     int num_pages, int page_size, uint8_t* k_codes, uint8_t* k_scales,
+                                     uint8_t* v_codes, uint8_t* v_scales, void* stream);
+
+/* Device workspace bytes of batq_attn_kv8 (independent of the batch and the lengths). Host only; no CUDA call. */
+BATQ_API batq_status batq_attn_kv8_workspace_size(int max_q_len, int q_heads, int kv_heads, int head_dim,
+                                                  size_t* bytes);
+
+/*
+ * Attention over that cache.  Query i of a sequence with n queries stands at
+ * token seq_lens[b] - n + i and sees the tokens up to its own:
+ *   out = sum_t p_t V_t,  p = softmax_t(softmax_scale * <q, K_t>)
+ * for each of q_heads heads; head h reads kv head h / (q_heads / kv_heads).
+ * One call serves decode steps (one query each), drafted tokens and short
+ * prompt chunks (the cost of long ones grows with their queries).
+ *
+ * Q: device, T rows of q_heads * head_dim elements (q_dtype), row stride ldq;
+ * out: the same of out_dtype, row stride ldo (16-byte multiples, 16-byte
+ * aligned).  max_q_len: the most queries of a sequence; queries of a longer
+ * sequence behind its first max_q_len are not computed.  lse: device, T x
+ * q_heads fp32 or NULL: log sum_t exp(softmax_scale * <q, K_t>).
+ * A query that sees no token (an empty sequence, or seq_lens[b] < n) gives
+ * zeros and lse = -inf; tokens of pages that are not named are not seen;
+ * seq_lens beyond the page table count as its end.  Rows of out and lse that
+ * belong to no sequence are not written.  What lies in the cache behind a
+ * sequence, or behind the tokens that a query sees, does not reach it, NaN
+ * included.
+ * Accuracy: queries are rounded to f16 after an exact normalisation (bf16
+ * queries lose nothing down to 2^-28 of the row's largest), probabilities to
+ * f16; scores, sums and outputs are fp32 until the last rounding.  The split
+ * of the work depends only on the lengths, so results repeat bit for bit.
+ * workspace: device, 16-byte aligned; calls that may overlap need one each.
+ * Errors: BATQ_ERR_INVALID_ARG (softmax_scale not finite), BATQ_ERR_SHAPE,
+ * BATQ_ERR_ALIGNMENT, BATQ_ERR_WORKSPACE, BATQ_ERR_ARCH, BATQ_ERR_CUDA.
+ */
+BATQ_API batq_status batq_attn_kv8(const void* Q, batq_dtype q_dtype, int T, int ldq, int q_heads, int kv_heads,
+                                   int head_dim, const int* cu_q_dev, const int* seq_lens_dev,
+                                   const int* page_table_dev, int batch, int max_pages, int num_pages, int page_size,
+                                   const uint8_t* k_codes, const uint8_t* k_scales, const uint8_t* v_codes,
+                                   const uint8_t* v_scales, float softmax_scale, int max_q_len, void* workspace,
+                                   size_t workspace_bytes, batq_dtype out_dtype, void* out, int ldo, float* lse,
+                                   void* stream);
+
+/*
+ * MXFP4 x MXFP4 products grouped by expert: rows [offsets[e], offsets[e + 1])
+ * of the activations times the weights of expert e,
+ *   out[r][m] = sum_n deq(a)[r][n] deq(w_e)[m][n].
+ * The offsets are read on the device, so a router's result needs no copy to
+ * the host.  Experts may have no rows.
+ *
+ * a_codes, a_scales: T rows sorted by expert, batq_quant_act's codes and
+ *    scales in the LINEAR layout (16-byte aligned).
+ * w_codes: E x M x N/2; w_scales: E consecutive MMA-layout buffers of M rows,
+ *    each batq_act_buffer_sizes(M, N, BATQ_SCALES_MMA) bytes.
+ * expert_offsets_dev: E + 1 ints, not decreasing, within [0, T] (values
+ *    outside are clamped, and one below an earlier one counts as that one).
+ * out: T rows of M elements, row stride ldo; rows outside every group are not
+ *    written.
+ * Errors: BATQ_ERR_INVALID_ARG, BATQ_ERR_SHAPE (E > 512, N % 64 != 0, M % 16
+ * != 0), BATQ_ERR_ALIGNMENT, BATQ_ERR_ARCH, BATQ_ERR_CUDA.
+ */
+BATQ_API batq_status batq_gemm_mxfp4_experts(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* w_codes,
+                                             const uint8_t* w_scales, const int* expert_offsets_dev, int E, int T,
+                                             int M, int N, batq_dtype out_dtype, void* out, int ldo, void* stream);
+
+/* Device workspace bytes of batq_linear_experts (the rows' codes and LINEAR scales). Host only; no CUDA call. */
+BATQ_API batq_status batq_linear_experts_workspace_size(int T, int N, size_t* bytes);
+
+/*
+ * The experts' linear of T sorted rows: batq_quant_act (one transform for all
+ * experts of the layer, LINEAR scales) into the workspace, then
+ * batq_gemm_mxfp4_experts, on one stream.  Errors as those, plus
+ * BATQ_ERR_WORKSPACE.
+ */
+BATQ_API batq_status batq_linear_experts(const void* X, batq_dtype x_dtype, int T, int N, int ldx,
+                                         const float* A_host, const float* B_dev, const float* ratios_dev,
+                                         const uint8_t* w_codes, const uint8_t* w_scales,
+                                         const int* expert_offsets_dev, int E, int M, void* workspace,
+                                         size_t workspace_bytes, batq_dtype out_dtype, void* out, int ldo,
+                                         void* stream);
+
 /*
  * Failure-path self-test: launches a one-thread kernel that waits on a
  * barrier nothing ever arrives on, with a bounded wait of `limit_us`

@@ -25,6 +25,8 @@ BATQ_SCALES_LINEAR = 0
 BATQ_SCALES_MMA = 1
 BATQ_KV_MXFP4 = 0
 BATQ_KV_MXFP8 = 1
+BATQ_W4_MXFP4 = 0
+BATQ_W4_NVFP4 = 1
 
 _c_int, _c_size_p, _vp, _fp = ctypes.c_int, ctypes.POINTER(ctypes.c_size_t), ctypes.c_void_p, ctypes.c_void_p
 
@@ -83,6 +85,19 @@ SIGNATURES = {
     "batq_rmsnorm_linear_workspace_size": (_c_int, [_c_int, _c_int, _c_size_p]),
     "batq_rmsnorm_linear": (_c_int, [_vp, _c_int, _c_int, _c_int, _c_int, _vp, ctypes.c_float, _vp, _vp, _vp, _vp,
                                      _vp, _c_int, _vp, ctypes.c_size_t, _c_int, _vp, _c_int, _vp]),
+    "batq_linear_w4a16": (_c_int, [_vp, _c_int, _c_int, _c_int, _c_int, _vp, _vp, _c_int, _vp, _vp, _vp, _c_int, _c_int,
+                                   _vp, _c_int, _vp]),
+    "batq_kv8_append": (_c_int, [_vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _vp, _vp, _c_int, _c_int,
+                                 _c_int, _c_int, _vp, _vp, _vp, _vp, _vp]),
+    "batq_attn_kv8_workspace_size": (_c_int, [_c_int, _c_int, _c_int, _c_int, _c_size_p]),
+    "batq_attn_kv8": (_c_int, [_vp, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _vp, _vp, _c_int, _c_int, _c_int,
+                               _c_int, _vp, _vp, _vp, _vp, ctypes.c_float, _c_int, _vp, ctypes.c_size_t, _c_int, _vp,
+                               _c_int, _vp, _vp]),
+    "batq_gemm_mxfp4_experts": (_c_int, [_vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _c_int,
+                                         _vp]),
+    "batq_linear_experts_workspace_size": (_c_int, [_c_int, _c_int, _c_size_p]),
+    "batq_linear_experts": (_c_int, [_vp, _c_int, _c_int, _c_int, _c_int, _vp, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int,
+                                     _vp, ctypes.c_size_t, _c_int, _vp, _c_int, _vp]),
     "batq_selftest_wait_timeout": (_c_int, [ctypes.c_uint, _vp]),
     "batq_device_error": (_c_int, [_vp, ctypes.POINTER(ctypes.c_uint)]),
 }

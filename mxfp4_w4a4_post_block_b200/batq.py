@@ -14,7 +14,7 @@ import numpy as np
 
 from . import _lib
 from ._lib import (BATQ_BF16, BATQ_F32, BATQ_KV_MXFP4, BATQ_KV_MXFP8, BATQ_OK, BATQ_SCALES_LINEAR,  # noqa: F401
-                   BATQ_SCALES_MMA)
+                   BATQ_SCALES_MMA, BATQ_W4_MXFP4, BATQ_W4_NVFP4)
 
 
 class BatqError(RuntimeError):
@@ -531,6 +531,150 @@ def batq_rmsnorm_linear(X, gamma, eps, A, B, ratios, w_codes, w_scales, M, works
                                            _dev_ptr(w_scales, "w_scales"), M, _dev_ptr(workspace, "workspace"),
                                            workspace.numel() * workspace.element_size(), _dtype_code(out),
                                            _dev_ptr(out, "out"), out.stride(0), _stream(stream)), "batq_rmsnorm_linear")
+
+
+# ------------------------------------------------------------ serving operators
+
+def _i32(t, name):
+    """Pointer of a contiguous int32 CUDA tensor (None -> NULL)."""
+    if t is not None and (t.dtype != _torch().int32 or not t.is_contiguous()):
+        raise TypeError(f"{name} must be a contiguous int32 tensor")
+    return _dev_ptr(t, name)
+
+
+def _u8(t, name, numel=None):
+    """Pointer of a contiguous uint8 CUDA tensor of `numel` elements at least."""
+    if t.dtype != _torch().uint8 or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous uint8 tensor")
+    if numel is not None and t.numel() < numel:
+        raise ValueError(f"{name} must hold {numel} bytes, got {t.numel()}")
+    return _dev_ptr(t, name)
+
+
+def _row_stride(t, cols, name):
+    """Row stride of a 2-D tensor whose rows hold `cols` consecutive elements."""
+    if t.dim() != 2 or t.shape[1] != cols or t.stride(1) != 1:
+        raise ValueError(f"{name} must be rows x {cols} with consecutive elements, got {tuple(t.shape)}")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), cols)
+
+
+def _lengths(cu, seq_lens, page_table, T):
+    """Batch size, after the shapes of a ragged batch's arrays."""
+    B = seq_lens.numel()
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError("page_table must be batch x max_pages")
+    if (cu.numel() != B + 1) if cu is not None else (T < B):
+        raise ValueError("cu must hold batch + 1 entries (without it, there must be a row per sequence)")
+    return B
+
+
+def _kv8_cache(k_codes, k_scales, v_codes, v_scales):
+    """(num_pages, kv_heads, page_size, head_dim) of a cache, after checking its four tensors."""
+    if k_codes.dim() != 4 or v_codes.shape != k_codes.shape:
+        raise ValueError("cache codes must be num_pages x kv_heads x page_size x head_dim, the same for K and V")
+    for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales")):
+        if tuple(t.shape) != tuple(k_codes.shape[:2]):
+            raise ValueError(f"{name} must be num_pages x kv_heads")
+    return tuple(k_codes.shape)
+
+
+def batq_linear_w4a16(X, A, B, w_codes, w_scales, M, out, w_gs=None, w_format=BATQ_W4_MXFP4, stream=None):
+    """out = (X P) W'^T of 1 to 16 tokens with prepared 4-bit weights (A = B = None: no transform)."""
+    S, N = X.shape
+    a = _host_f32(A, 64, "A") if A is not None else None
+    if B is not None and (B.dtype != _torch().float32 or not B.is_contiguous() or B.numel() < N // 32 * 16):
+        raise ValueError("B must hold N / 32 x 16 contiguous floats")
+    if tuple(out.shape) != (S, M):
+        raise ValueError(f"out must be {S} x {M}")
+    lib = _lib.load()
+    _check(lib.batq_linear_w4a16(_dev_ptr(X, "X"), _dtype_code(X), S, N, _row_stride(X, N, "X"),
+                                 a.ctypes.data if a is not None else None, _dev_ptr(B, "B"), w_format,
+                                 _u8(w_codes, "w_codes", M * N // 2), _u8(w_scales, "w_scales"), _dev_ptr(w_gs, "w_gs"), M,
+                                 _dtype_code(out), _dev_ptr(out, "out"), _row_stride(out, M, "out"), _stream(stream)),
+           "batq_linear_w4a16")
+
+
+def batq_kv8_append(K, V, cu_new, seq_lens, page_table, k_codes, k_scales, v_codes, v_scales, stream=None):
+    """New K and V rows (T x kv_heads * head_dim) into the 8-bit paged cache; cu_new None: one per sequence."""
+    P, H, page, D = _kv8_cache(k_codes, k_scales, v_codes, v_scales)
+    T = K.shape[0]
+    B = _lengths(cu_new, seq_lens, page_table, T)
+    if V.shape != K.shape or V.dtype != K.dtype:
+        raise ValueError("K and V must have the same shape and type")
+    _check(_lib.load().batq_kv8_append(_dev_ptr(K, "K"), _dev_ptr(V, "V"), _dtype_code(K), T, H, D,
+                                       _row_stride(K, H * D, "K"), _row_stride(V, H * D, "V"), _i32(cu_new, "cu_new"),
+                                       _i32(seq_lens, "seq_lens"), _i32(page_table, "page_table"), B,
+                                       page_table.shape[1], P, page, _u8(k_codes, "k_codes"), _u8(k_scales, "k_scales"),
+                                       _u8(v_codes, "v_codes"), _u8(v_scales, "v_scales"), _stream(stream)),
+           "batq_kv8_append")
+
+
+def batq_attn_kv8_workspace_size(max_q_len: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
+    b = ctypes.c_size_t()
+    _check(_lib.load().batq_attn_kv8_workspace_size(max_q_len, q_heads, kv_heads, head_dim, ctypes.byref(b)),
+           "batq_attn_kv8_workspace_size")
+    return b.value
+
+
+def batq_attn_kv8(Q, cu_q, seq_lens, page_table, k_codes, k_scales, v_codes, v_scales, softmax_scale, max_q_len,
+                  workspace, out, lse=None, stream=None):
+    """Attention of Q (T x q_heads * head_dim) over the 8-bit paged cache; cu_q None: one query per sequence."""
+    P, H, page, D = _kv8_cache(k_codes, k_scales, v_codes, v_scales)
+    T, row = Q.shape
+    B = _lengths(cu_q, seq_lens, page_table, T)
+    if row % D or tuple(out.shape) != (T, row):
+        raise ValueError("Q and out must be T x q_heads * head_dim")
+    if lse is not None and (lse.dtype != _torch().float32 or not lse.is_contiguous() or tuple(lse.shape) != (T, row // D)):
+        raise ValueError("lse must be a contiguous fp32 tensor, T x q_heads")
+    _check(_lib.load().batq_attn_kv8(_dev_ptr(Q, "Q"), _dtype_code(Q), T, _row_stride(Q, row, "Q"), row // D, H, D,
+                                     _i32(cu_q, "cu_q"), _i32(seq_lens, "seq_lens"), _i32(page_table, "page_table"), B,
+                                     page_table.shape[1], P, page, _u8(k_codes, "k_codes"), _u8(k_scales, "k_scales"),
+                                     _u8(v_codes, "v_codes"), _u8(v_scales, "v_scales"), softmax_scale, max_q_len,
+                                     _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(),
+                                     _dtype_code(out), _dev_ptr(out, "out"), _row_stride(out, row, "out"),
+                                     _dev_ptr(lse, "lse"), _stream(stream)), "batq_attn_kv8")
+
+
+def empty_kv8_cache(num_pages: int, kv_heads: int, page_size: int, head_dim: int, device="cuda"):
+    """(k_codes, k_scales, v_codes, v_scales) of an 8-bit paged cache."""
+    torch = _torch()
+    codes = [torch.empty(num_pages, kv_heads, page_size, head_dim, dtype=torch.uint8, device=device) for _ in range(2)]
+    scales = [torch.empty(num_pages, kv_heads, dtype=torch.uint8, device=device) for _ in range(2)]
+    return codes[0], scales[0], codes[1], scales[1]
+
+
+def batq_gemm_mxfp4_experts(a_codes, a_scales, w_codes, w_scales, expert_offsets, M, N, out, stream=None):
+    """Rows [offsets[e], offsets[e + 1]) of a (LINEAR scales) times expert e's weights (E x M x N/2)."""
+    T, E = a_codes.shape[0], expert_offsets.numel() - 1
+    if tuple(out.shape) != (T, M):
+        raise ValueError(f"out must be {T} x {M}")
+    _check(_lib.load().batq_gemm_mxfp4_experts(_u8(a_codes, "a_codes", T * N // 2), _u8(a_scales, "a_scales", T * N // 32),
+                                               _u8(w_codes, "w_codes", E * M * N // 2), _u8(w_scales, "w_scales"),
+                                               _i32(expert_offsets, "expert_offsets"), E, T, M, N, _dtype_code(out),
+                                               _dev_ptr(out, "out"), _row_stride(out, M, "out"), _stream(stream)),
+           "batq_gemm_mxfp4_experts")
+
+
+def batq_linear_experts_workspace_size(T: int, N: int) -> int:
+    b = ctypes.c_size_t()
+    _check(_lib.load().batq_linear_experts_workspace_size(T, N, ctypes.byref(b)), "batq_linear_experts_workspace_size")
+    return b.value
+
+
+def batq_linear_experts(X, A, B, ratios, w_codes, w_scales, expert_offsets, M, workspace, out, stream=None):
+    """Quantiser and experts' products of the sorted rows X (T x N) on one stream."""
+    T, N = X.shape
+    E = expert_offsets.numel() - 1
+    a = _host_f32(A, 64, "A")
+    if tuple(out.shape) != (T, M):
+        raise ValueError(f"out must be {T} x {M}")
+    _check(_lib.load().batq_linear_experts(_dev_ptr(X, "X"), _dtype_code(X), T, N, _row_stride(X, N, "X"), a.ctypes.data,
+                                           _dev_ptr(B, "B"), _dev_ptr(ratios, "ratios"),
+                                           _u8(w_codes, "w_codes", E * M * N // 2), _u8(w_scales, "w_scales"),
+                                           _i32(expert_offsets, "expert_offsets"), E, M, _dev_ptr(workspace, "workspace"),
+                                           workspace.numel() * workspace.element_size(), _dtype_code(out),
+                                           _dev_ptr(out, "out"), _row_stride(out, M, "out"), _stream(stream)),
+           "batq_linear_experts")
 
 
 def batq_selftest_wait_timeout(limit_us: int, stream=None):

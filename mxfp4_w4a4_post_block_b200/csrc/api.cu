@@ -290,6 +290,11 @@ batq_status launch_rmsnorm_quant(const void* X, batq_dtype x_dtype, int S, int N
 
 }  // namespace
 
+namespace batq {
+int arch_status() { return check_arch(); }
+unsigned* device_error_word() { return error_word(); }
+}  // namespace batq
+
 extern "C" {
 
 const char* batq_status_string(batq_status status) {

@@ -2,9 +2,14 @@
 #pragma once
 
 #include <cuda_runtime.h>
+#include <cstddef>
 #include <cstdint>
 
 namespace batq {
+
+// The current device's check (a batq_status) and error word, shared by the files of the C ABI.
+int arch_status();
+unsigned* device_error_word();
 
 // Element / scale format of a quantised operand.
 enum Fmt : int {
@@ -117,6 +122,88 @@ cudaError_t launch_e2m1_to_e4m3(const uint8_t* packed, uint8_t* out, size_t pack
 // fp64); X as for the quantisers (16-byte aligned rows).
 cudaError_t launch_row_rms(const void* X, bool bf16, int S, int N, int ldx, float eps, float* r_out,
                            cudaStream_t stream);
+
+// New K and V rows into the pages of an 8-bit cache (kv8.cuh).  Row r of K (V) starts ldk (ldv)
+// elements after row r - 1 and holds kv_heads * head_dim elements.
+struct Kv8AppendLaunch {
+  const void* K;
+  const void* V;
+  bool bf16;
+  int T, kv_heads, head_dim, ldk, ldv;
+  const int* cu_new;      // device [batch + 1], or nullptr: one token per sequence
+  const int* seq_lens;    // device [batch]: tokens with the new ones
+  const int* page_table;  // device [batch][max_pages]
+  int batch, max_pages, num_pages, page_size;
+  uint8_t* k_codes;
+  uint8_t* k_scales;
+  uint8_t* v_codes;
+  uint8_t* v_scales;
+};
+cudaError_t launch_kv8_append(const Kv8AppendLaunch& L, cudaStream_t stream);
+
+// Attention of ragged queries over that cache.
+struct AttnKv8Launch {
+  const void* Q;
+  bool q_bf16;
+  int T, ldq, q_heads, kv_heads, head_dim;
+  const int* cu_q;        // device [batch + 1], or nullptr: one query per sequence
+  const int* seq_lens;
+  const int* page_table;
+  int batch, max_pages, num_pages, page_size;
+  const uint8_t* k_codes;
+  const uint8_t* k_scales;
+  const uint8_t* v_codes;
+  const uint8_t* v_scales;
+  float softmax_scale;
+  int max_q_len;
+  float* workspace;
+  bool out_bf16;
+  void* out;
+  int ldo;
+  float* lse;             // device [T][q_heads], or nullptr
+  unsigned* err;
+};
+size_t attn_kv8_workspace_bytes(int max_q_len, int q_heads, int kv_heads, int head_dim);
+// cudaErrorInvalidValue when a tensor map cannot be encoded.
+cudaError_t launch_attn_kv8(const AttnKv8Launch& L, cudaStream_t stream);
+
+// Products of few tokens with prepared 4-bit weights, activations not quantised.
+struct LinearW4A16Launch {
+  const void* X;
+  bool x_bf16;
+  int S, N, ldx;
+  bool transform;        // A and B are set
+  float A[64];
+  const float* B;        // device, k x 16
+  bool nvfp4;
+  const uint8_t* w_codes;
+  const uint8_t* w_scales;  // MMA layout, M rows
+  const float* w_gs;     // NVFP4: device float, or nullptr (1)
+  int M;
+  bool out_bf16;
+  void* out;
+  int ldo;
+  unsigned* err;
+};
+constexpr int kMaxW4A16Tokens = 16;
+constexpr int kMaxW4A16N = 131072;
+cudaError_t launch_linear_w4a16(const LinearW4A16Launch& L, cudaStream_t stream);
+
+// Products of the ragged row groups of E experts, MXFP4 x MXFP4.
+struct ExpertsLaunch {
+  const uint8_t* a_codes;
+  const uint8_t* a_scales;  // LINEAR layout, T rows
+  const uint8_t* w_codes;   // E x M x N/2
+  const uint8_t* w_scales;  // E x (MMA layout, M rows)
+  const int* offsets;       // device [E + 1]
+  int E, T, M, N;
+  bool out_bf16;
+  void* out;
+  int ldo;
+  unsigned* err;
+};
+constexpr int kMaxExperts = 512;
+cudaError_t launch_gemm_experts(const ExpertsLaunch& L, cudaStream_t stream);
 
 // One-thread kernel whose barrier wait always expires after limit_ns.
 cudaError_t launch_wait_selftest(uint64_t limit_ns, unsigned* err, cudaStream_t stream);

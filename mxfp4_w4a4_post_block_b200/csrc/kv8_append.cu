@@ -1,0 +1,181 @@
+// k_kv8_append: new K and V rows into the pages of an 8-bit cache with one scale per (page, kv head).
+//
+// A block of the cache is one head's rows of one page.  Its scale is 2^e with the smallest e that
+// covers every finite value written to the block so far (amax <= 448 * 2^e, so nothing saturates);
+// codes are E4M3_RNE(x * 2^-e).  A power of two costs E4M3 no precision (its step is relative) and
+// makes the scale's growth exact: when a later token needs a larger e, the block's older codes are
+// multiplied by 2^(e_old - e) and rounded again, which is exact down to the E4M3 subnormals.  The
+// first token of a page sets the scale afresh, whatever the page held before.  NaN and infinities
+// are stored as the E4M3 NaN and take no part in the amax.
+//
+// One CTA owns one block that receives tokens (blockIdx.x: the touched pages of the batch in order;
+// y: kv head; z: K or V), so no block has two writers and the result does not depend on order.  Rows
+// are read twice (amax, then codes); the second read hits L1/L2.
+#include <cstdint>
+
+#include "kernels.h"
+#include "kv8.cuh"
+#include "ptx.cuh"
+
+namespace batq {
+namespace {
+
+constexpr int kThreads = 128;
+
+// Smallest e >= -127 with |a| <= 448 * 2^e (448 = 1.75 * 2^8), a finite and >= 0.
+__device__ __forceinline__ int block_exponent(float a) {
+  const uint32_t u = __float_as_uint(a);
+  const int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  return max(e, -127);
+}
+
+__device__ __forceinline__ float finite_or_nan(float v) {
+  return fabsf(v) <= 3.402823466e38f ? v : __uint_as_float(0x7FC00000u);
+}
+
+// Eight consecutive elements of a row.
+template <bool kBF16>
+__device__ __forceinline__ void load8(const uint8_t* p, float (&v)[8]) {
+  if constexpr (kBF16) {
+    const uint4 q = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  } else {
+    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 16);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+}
+
+template <bool kBF16>
+__global__ void __launch_bounds__(kThreads) k_kv8_append(const Kv8AppendLaunch a) {
+  __shared__ int s_seq, s_page;
+  __shared__ float s_amax[kThreads / 32];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int max_len = a.max_pages * a.page_size;
+
+  // The blockIdx.x-th touched page: sequence b with new tokens at positions len - count .. len - 1.
+  if (tid < 32) {
+    int before = 0, seq = -1, page = 0;
+    for (int b0 = 0; b0 < a.batch && seq < 0; b0 += 32) {
+      const int b = b0 + lane;
+      int first = 0, n = 0;
+      if (b < a.batch) {
+        const SeqRows s = seq_rows(a.cu_new, a.seq_lens, b, a.T, max_len);
+        if (s.count > 0 && a.seq_lens[b] >= s.count) {  // tokens past the page table are dropped
+          first = (a.seq_lens[b] - s.count) / a.page_size;
+          n = max(0, (s.len - 1) / a.page_size - first + 1);
+        }
+      }
+      int incl = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      const int at = (int)blockIdx.x - before - (incl - n);
+      const unsigned hit = __ballot_sync(0xffffffffu, at >= 0 && at < n);
+      if (hit) {
+        const int src = __ffs(hit) - 1;
+        seq = b0 + src;
+        page = __shfl_sync(0xffffffffu, first + at, src);
+      }
+      before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) {
+      s_seq = seq;
+      s_page = page;
+    }
+  }
+  __syncthreads();
+  const int b = s_seq;
+  if (b < 0) return;
+  const int pid = a.page_table[(size_t)b * a.max_pages + s_page];
+  if (pid < 0 || pid >= a.num_pages) return;
+  const SeqRows s = seq_rows(a.cu_new, a.seq_lens, b, a.T, max_len);
+  const int pos0 = a.seq_lens[b] - s.count;                      // position of the sequence's first new token
+  const int begin = max(pos0, s_page * a.page_size);             // this page's new positions
+  const int end = min(s.len, (s_page + 1) * a.page_size);
+  const int off0 = begin - s_page * a.page_size;                 // rows that were there before
+  const int h = blockIdx.y;
+  const bool is_v = blockIdx.z != 0;
+  const int D = a.head_dim, per_row = D >> 3, chunks = (end - begin) * per_row;
+  constexpr size_t esz = kBF16 ? 2 : 4;
+  const size_t ld = (size_t)(is_v ? a.ldv : a.ldk) * esz;
+  const uint8_t* x = static_cast<const uint8_t*>(is_v ? a.V : a.K) + (size_t)(s.begin + begin - pos0) * ld +
+                     (size_t)h * D * esz;
+  const size_t block = (size_t)pid * a.kv_heads + h;
+  uint8_t* codes = (is_v ? a.v_codes : a.k_codes) + block * ((size_t)a.page_size * D);
+  uint8_t* scale = (is_v ? a.v_scales : a.k_scales) + block;
+
+  float amax = 0.0f;
+  for (int c = tid; c < chunks; c += kThreads) {
+    float v[8];
+    load8<kBF16>(x + (size_t)(c / per_row) * ld + (size_t)(c % per_row) * 8 * esz, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float m = fabsf(v[i]);
+      amax = m <= 3.402823466e38f ? fmaxf(amax, m) : amax;
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  if (lane == 0) s_amax[tid >> 5] = amax;
+  const int e_old = off0 > 0 ? (int)*scale - 127 : -127;
+  __syncthreads();  // also: every thread has the old scale before it is replaced
+  amax = s_amax[0];
+#pragma unroll
+  for (int i = 1; i < kThreads / 32; ++i) amax = fmaxf(amax, s_amax[i]);
+  const int e = max(e_old, block_exponent(amax));
+  if (tid == 0) *scale = (uint8_t)(e + 127);
+
+  if (e > e_old && off0 > 0) {
+    const float f = e8m0_value((uint32_t)max(127 + e_old - e, 0));
+    uint4* old = reinterpret_cast<uint4*>(codes);
+    for (int c = tid; c < off0 * D / 16; c += kThreads) {
+      const uint4 q = old[c];
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+      uint32_t r[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 lo = e4m3x2_values(w[i] & 0xFFFFu), hi = e4m3x2_values(w[i] >> 16);
+        r[i] = e4m3x4(lo.x * f, lo.y * f, hi.x * f, hi.y * f);
+      }
+      old[c] = make_uint4(r[0], r[1], r[2], r[3]);
+    }
+  }
+  const float inv = e8m0_value((uint32_t)max(127 - e, 0));  // 2^-e
+  uint8_t* dst = codes + (size_t)off0 * D;
+  for (int c = tid; c < chunks; c += kThreads) {
+    float v[8];
+    load8<kBF16>(x + (size_t)(c / per_row) * ld + (size_t)(c % per_row) * 8 * esz, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = finite_or_nan(v[i]) * inv;
+    reinterpret_cast<uint2*>(dst)[c] = make_uint2(e4m3x4(v[0], v[1], v[2], v[3]), e4m3x4(v[4], v[5], v[6], v[7]));
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_kv8_append(const Kv8AppendLaunch& L, cudaStream_t stream) {
+  // A sequence with n >= 1 new tokens touches at most min(n, n / page + 2) pages.
+  const long long items = (long long)L.T / L.page_size + 2LL * L.batch;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(items < L.T ? items : L.T), (unsigned)L.kv_heads, 2);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return L.bf16 ? cudaLaunchKernelEx(&cfg, k_kv8_append<true>, L) : cudaLaunchKernelEx(&cfg, k_kv8_append<false>, L);
+}
+
+}  // namespace batq

@@ -1,0 +1,531 @@
+"""GPU parity of the serving operators (4-bit weight products of few tokens, 8-bit paged cache and its
+attention, products grouped by expert) against their definitions in fp64."""
+
+import numpy as np
+import pytest
+import torch
+
+from mxfp4_w4a4_post_block_b200 import batq as BQ
+import serving_ref as R
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def ok():
+    assert BQ.batq_device_error() == 0
+
+
+def host(t):
+    return t.double().cpu().numpy()
+
+
+# ------------------------------------------------------------------ W4A16
+
+def w4a16_case(S, N, M, fmt, x_dtype, tr, seed, x=None, lin=None):
+    rng = np.random.default_rng(seed)
+    codes, lin0 = R.random_weights(rng, M, N, fmt)
+    lin = lin0 if lin is None else lin(lin0)
+    x = torch.from_numpy((rng.standard_normal((S, N)) * np.exp(rng.standard_normal((S, 1)))).astype(np.float32)) if x is None else x
+    x = x.to(x_dtype)
+    A = (np.eye(8) + 0.1 * rng.standard_normal((8, 8))).astype(np.float32) if tr else None
+    B = (np.eye(4) + 0.1 * rng.standard_normal((N // 32, 4, 4))).astype(np.float32) if tr else None
+    return x, A, B, codes, lin, rng
+
+
+def w4a16_run(x, A, B, codes, lin, fmt, out_dtype, gs=None):
+    out = torch.full((x.shape[0], codes.shape[0]), 7.0, dtype=out_dtype, device="cuda")
+    BQ.batq_linear_w4a16(x.cuda(), A, R.cuda(B) if B is not None else None, R.cuda(codes), R.cuda(R.tile_scales(lin)),
+                         codes.shape[0], out, w_gs=gs,
+                         w_format=BQ.BATQ_W4_MXFP4 if fmt == "mxfp4" else BQ.BATQ_W4_NVFP4)
+    ok()
+    return out
+
+
+def w4a16_check(out, x, A, B, codes, lin, fmt, gs=1.0):
+    N = x.shape[1]
+    xd = x.double().numpy()
+    y, cond = R.transform(xd, A, B) if A is not None else (xd, np.abs(xd))
+    w = R.weights(codes, lin, fmt)
+    ref = y @ w.T / gs
+    # fp32 transform (12 roundings, half a step each), y to 22 bits and 2^-39 of the token's largest, and one fp32
+    # rounding (two half steps: the tensor core truncates) per 16 products and per scaled partial sum.
+    each = cond * (12 * 2.0 ** -24 + 2.0 ** -22) + np.abs(y).max(1, keepdims=True) * 2.0 ** -38
+    tol = (each + np.abs(y) * ((N / 8 + 24) * 2.0 ** -23)) @ np.abs(w).T / gs
+    tol += np.abs(ref) * (2.0 ** -8 if out.dtype == BF else 2.0 ** -23)
+    err = np.abs(host(out) - ref)
+    assert (err <= tol).all(), (err / np.maximum(tol, 1e-300)).max()
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("S,N,M,x_dtype,out_dtype,tr", [
+    (1, 64, 16, BF, F32, False), (1, 256, 128, F32, F32, True), (2, 320, 48, BF, BF, True), (3, 2112, 144, BF, F32, True),
+    (4, 1024, 1040, F32, BF, False), (7, 4096, 96, BF, F32, False), (8, 512, 272, F32, F32, True),
+    (13, 1088, 160, BF, F32, False), (16, 2048, 64, F32, F32, True), (16, 4160, 528, BF, BF, True),
+])
+def test_w4a16_shapes(S, N, M, x_dtype, out_dtype, tr, fmt):
+    x, A, B, codes, lin, _ = w4a16_case(S, N, M, fmt, x_dtype, tr, S + N)
+    w4a16_check(w4a16_run(x, A, B, codes, lin, fmt, out_dtype), x, A, B, codes, lin, fmt)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("S,N,tr", [(1, 32768, True), (16, 12288, True), (16, 20480, False), (9, 33024, True)])
+def test_w4a16_long_rows_split_over_a_cluster(S, N, tr, fmt):
+    x, A, B, codes, lin, _ = w4a16_case(S, N, 32, fmt, BF, tr, S + N)
+    w4a16_check(w4a16_run(x, A, B, codes, lin, fmt, F32), x, A, B, codes, lin, fmt)
+
+
+def test_w4a16_many_units_and_tensor_scale():
+    x, A, B, codes, lin, _ = w4a16_case(2, 768, 24576, "nvfp4", BF, True, 5)
+    gs = torch.tensor([37.5], device="cuda")
+    w4a16_check(w4a16_run(x, A, B, codes, lin, "nvfp4", F32, gs), x, A, B, codes, lin, "nvfp4", 37.5)
+
+
+def test_w4a16_equals_prepared_weights_of_the_library():
+    """Weights of batq_prepare_weights: x P (W P^-T)^T is x W^T up to the weights' own rounding, and equals the
+    product with the decoded codes."""
+    rng = np.random.default_rng(3)
+    M, N = 256, 512
+    W = torch.from_numpy((rng.standard_normal((M, N)) * 0.02).astype(np.float32)).cuda()
+    A = (np.eye(8) + 0.1 * rng.standard_normal((8, 8))).astype(np.float32)
+    B = (np.eye(4) + 0.1 * rng.standard_normal((N // 32, 4, 4))).astype(np.float32)
+    lin_codes, lin = BQ.empty_act_buffers(M, N, BQ.BATQ_SCALES_LINEAR)
+    codes, scales = BQ.empty_act_buffers(M, N)
+    ws = torch.empty(BQ.batq_prepare_workspace_size(N), dtype=torch.uint8, device="cuda")
+    BQ.batq_prepare_weights(W, A, B, lin_codes, lin, ws, BQ.BATQ_SCALES_LINEAR)
+    BQ.batq_prepare_weights(W, A, B, codes, scales, ws)
+    x = torch.from_numpy(rng.standard_normal((3, N)).astype(np.float32))
+    out = torch.empty(3, M, device="cuda")
+    BQ.batq_linear_w4a16(x.cuda(), A, R.cuda(B), codes, scales, M, out)
+    ok()
+    w4a16_check(out, x, A, B, lin_codes.cpu().numpy(), lin.cpu().numpy().reshape(M, -1), "mxfp4")
+    plain = host(x @ W.cpu().T.float())
+    assert np.linalg.norm(host(out) - plain) < 0.2 * np.linalg.norm(plain)
+
+
+@pytest.mark.parametrize("mag", [1e-38, 1e-30, 1e30])
+@pytest.mark.parametrize("tr", [False, True])
+def test_w4a16_magnitudes_of_tokens(mag, tr):
+    """Tokens far from 1: normalisation is per token, so one does not disturb another."""
+    x, A, B, codes, lin, rng = w4a16_case(4, 256, 64, "mxfp4", F32, tr, 8)
+    x[1] *= mag
+    x[2] = 0.0
+    out = w4a16_run(x, A, B, codes, lin, "mxfp4", F32)
+    assert (out[2] == 0).all()
+    if mag < 1e-35:  # subnormal sums: absolute steps of 2^-149 and flushed terms
+        keep = [0, 2, 3]
+        assert torch.isfinite(out).all()
+        w4a16_check(out[keep], x[keep], A, B, codes, lin, "mxfp4")
+    else:
+        w4a16_check(out, x, A, B, codes, lin, "mxfp4")
+
+
+def test_w4a16_non_finite_values_stay_with_their_token_and_row():
+    x, A, B, codes, lin, _ = w4a16_case(4, 256, 64, "mxfp4", BF, False, 9)
+    clean = w4a16_run(x, A, B, codes, lin, "mxfp4", F32)
+    x[1, 7], x[3, 200] = float("nan"), float("inf")
+    lin[5, 3] = 255   # a weight row with a NaN scale
+    lin[9, 2] = 0     # and one with the smallest scale
+    out = w4a16_run(x, A, B, codes, lin, "mxfp4", F32)
+    assert out[1].isnan().all() and not out[3].isfinite().any() and out[:, 5].isnan().all()
+    same = [m for m in range(64) if m not in (5, 9)]
+    assert torch.equal(out[0][same], clean[0][same]) and torch.equal(out[2][same], clean[2][same])
+    w = R.weights(codes, lin, "mxfp4")
+    assert abs(float(out[0, 9]) - float(x[0].double().numpy() @ w[9])) < 1e-4
+
+
+def test_w4a16_strides_and_untouched_columns():
+    x, A, B, codes, lin, rng = w4a16_case(5, 320, 48, "mxfp4", BF, True, 10)
+    big = torch.full((5, 320 + 64), float("nan"), dtype=BF, device="cuda")
+    big[:, 32:352] = x.cuda()
+    out = torch.full((5, 64), 3.0, device="cuda")
+    BQ.batq_linear_w4a16(big[:, 32:352], A, R.cuda(B), R.cuda(codes), R.cuda(R.tile_scales(lin)), 48, out[:, 8:56])
+    ok()
+    w4a16_check(out[:, 8:56], x, A, B, codes, lin, "mxfp4")
+    assert (out[:, :8] == 3).all() and (out[:, 56:] == 3).all()
+
+
+# ------------------------------------------------------------------ the cache
+
+def ragged(rng, B, most_new, most_old, page, spare=3, shuffle=True):
+    new = rng.integers(0, most_new + 1, B)
+    new[0] = max(new[0], 1)
+    lens = new + rng.integers(0, most_old + 1, B)
+    need = (lens + page - 1) // page
+    pages = int(need.sum()) + spare
+    ids = rng.permutation(pages) if shuffle else np.arange(pages)
+    table = np.full((B, int(need.max()) + 1), -1, np.int32)
+    at = 0
+    for b in range(B):
+        table[b, :need[b]] = ids[at:at + need[b]]
+        at += need[b]
+    cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    return cu, lens.astype(np.int32), table, pages
+
+
+def append_run(K, V, cu, lens, table, kc, ks, vc, vs):
+    t = [R.cuda(a) for a in (kc, ks, vc, vs)]
+    BQ.batq_kv8_append(K, V, R.cuda(cu) if cu is not None else None, R.cuda(lens), R.cuda(table), *t)
+    ok()
+    return [a.cpu().numpy() for a in t]
+
+
+def append_check(x, cu, lens, table, page, codes, scales, got_codes, got_scales):
+    vals, exps = R.e4m3_value(codes), scales.astype(np.int64) - 127
+    R.append(x, cu, lens, table, page, vals, exps)
+    np.testing.assert_array_equal(got_scales.astype(np.int64) - 127, exps)
+    np.testing.assert_array_equal(R.e4m3_value(got_codes), vals)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("page,D,heads,B,new,old", [(16, 128, 8, 9, 1, 60), (16, 64, 1, 4, 40, 20), (32, 256, 3, 5, 70, 50),
+                                                    (64, 128, 2, 40, 3, 200), (128, 64, 2, 3, 300, 130)])
+def test_append_exact(page, D, heads, B, new, old, dtype):
+    rng = np.random.default_rng(page + D)
+    cu, lens, table, pages = ragged(rng, B, new, old, page)
+    T = int(cu[-1])
+    kc, ks = R.cache(rng, pages, heads, page, D)
+    vc, vs = R.cache(rng, pages, heads, page, D)
+    # values of very different sizes, so that many scales grow and many do not
+    x = torch.from_numpy((rng.standard_normal((T + 2, 2 * heads * D)) * np.exp2(rng.integers(-9, 4, (T + 2, 1)))).astype(np.float32)).to(dtype)
+    K, V = x.cuda()[:, :heads * D], x.cuda()[:, heads * D:]
+    g = append_run(K, V, cu, lens, table, kc, ks, vc, vs)
+    xs = x.double().numpy()
+    append_check(xs[:, :heads * D].reshape(-1, heads, D), cu, lens, table, page, kc, ks, g[0], g[1])
+    append_check(xs[:, heads * D:].reshape(-1, heads, D), cu, lens, table, page, vc, vs, g[2], g[3])
+
+
+def test_append_token_by_token_and_extremes():
+    """One token a call (cu None): zeros, subnormals, the largest bf16, NaN and infinities, growing scales."""
+    rng = np.random.default_rng(1)
+    page, heads, D, B = 16, 2, 64, 3
+    table = np.array([[5, 1], [0, 3], [2, 4]], np.int32)
+    kc, ks = R.cache(rng, 6, heads, page, D)
+    vc, vs = R.cache(rng, 6, heads, page, D)
+    mags = [0.0, 1e-40, 1e-38, 1e-3, 1.0, 3e38, 1.0, 448.0, 449.0]
+    for n, mag in enumerate(mags):
+        x = (rng.uniform(-1, 1, (B, heads * D)) * mag).astype(np.float32)
+        if n == 4:
+            x[1, 3], x[1, 70], x[2, 5] = np.nan, np.inf, -np.inf
+        xb = torch.from_numpy(x).to(BF)
+        lens = np.array([n + 1, n + 15, n + 20], np.int32)
+        cu = np.arange(B + 1)
+        g = append_run(xb.cuda(), xb.cuda(), None, lens, table, kc, ks, vc, vs)
+        xs = xb.double().numpy().reshape(B, heads, D)
+        append_check(xs, cu, lens, table, page, kc, ks, g[0], g[1])
+        append_check(xs, cu, lens, table, page, vc, vs, g[2], g[3])
+        kc, ks, vc, vs = g
+
+
+def test_append_drops_what_has_no_place():
+    """Unnamed pages, lengths behind the page table, decreasing and outside ranges, fewer tokens than rows."""
+    rng = np.random.default_rng(2)
+    page, heads, D = 16, 2, 64
+    table = np.array([[0, 99], [-1, 1], [2, 3], [4, 5], [6, 7]], np.int32)
+    cu = np.array([0, 20, 45, 65, 60, 70], np.int32)   # sequence 3's range decreases
+    lens = np.array([25, 25, 40, 30, 3], np.int32)     # sequence 2 outgrows its table, 4 has fewer tokens than rows
+    T = 70
+    kc, ks = R.cache(rng, 8, heads, page, D)
+    vc, vs = R.cache(rng, 8, heads, page, D)
+    x = torch.from_numpy(rng.standard_normal((T, heads * D)).astype(np.float32))
+    g = append_run(x.cuda(), x.cuda(), cu, lens, table, kc, ks, vc, vs)
+    append_check(x.double().numpy().reshape(T, heads, D), cu, lens, table, page, kc, ks, g[0], g[1])
+    append_check(x.double().numpy().reshape(T, heads, D), cu, lens, table, page, vc, vs, g[2], g[3])
+
+
+# ------------------------------------------------------------------ attention
+
+def attn_run(q, cu, lens, table, kc, ks, vc, vs, scale, max_q, out_dtype=BF, lse=True, heads=None):
+    T, row = q.shape
+    D, kv = kc.shape[3], kc.shape[1]
+    out = torch.full((T, row), 7.0, dtype=out_dtype, device="cuda")
+    l = torch.full((T, row // D), 7.0, device="cuda") if lse else None
+    ws = torch.full((BQ.batq_attn_kv8_workspace_size(max_q, row // D, kv, D),), 255, dtype=torch.uint8, device="cuda")
+    BQ.batq_attn_kv8(q.cuda(), R.cuda(cu) if cu is not None else None, R.cuda(lens), R.cuda(table), R.cuda(kc), R.cuda(ks),
+                     R.cuda(vc), R.cuda(vs), scale, max_q, ws, out, lse=l)
+    ok()
+    return out, l
+
+
+def attn_check(out, lse, q, cu, lens, table, kc, ks, vc, vs, scale, max_q):
+    T = q.shape[0]
+    page, D = kc.shape[2:]
+    k = R.e4m3_value(kc) * R.e8m0_value(ks)[..., None, None]
+    v = R.e4m3_value(vc) * R.e8m0_value(vs)[..., None, None]
+    qd = q.double().numpy().reshape(T, -1, D)
+    ref, rlse, tol = R.attention(qd, cu, lens, table, page, k, v, R.e8m0_value(vs), scale, max_q, 23 if q.dtype == BF else 11)
+    got, mine = host(out).reshape(ref.shape), ~np.isnan(tol).all(2)
+    assert (got[~mine] == 7).all(), "rows of no sequence were written"
+    tol = tol + np.abs(ref) * (2.0 ** -8 if out.dtype == BF else 2.0 ** -22) + 2.0 ** -140
+    err = np.abs(got - ref)[mine]
+    assert (err <= tol[mine]).all(), (err / tol[mine]).max()
+    if lse is not None:
+        l = host(lse)
+        assert (l[~mine] == 7).all()
+        empty = mine & np.isneginf(rlse)
+        assert np.isneginf(l[empty]).all() and (got[empty] == 0).all()
+        m = mine & ~empty
+        assert np.abs(l - rlse)[m].max(initial=0) < 2e-3 * (1 + np.abs(rlse[m]).max(initial=0))
+
+
+def attn_case(seed, B, kv, G, D, page, most, q_most, q_dtype=BF, pad=0, spread=1.0, cu_given=True):
+    rng = np.random.default_rng(seed)
+    cu, lens, table, pages = ragged(rng, B, q_most, most, page)
+    if not cu_given:
+        lens = np.maximum(lens - np.diff(cu) + 1, 0).astype(np.int32)
+        cu = np.arange(B + 1).astype(np.int32)
+        table = np.where(np.arange(table.shape[1])[None] * page < lens[:, None], table, -1).astype(np.int32)
+        need = (lens + page - 1) // page
+        at = rng.permutation(pages + B)
+        pages += B
+        i = 0
+        for b in range(B):
+            table[b, :need[b]] = at[i:i + need[b]]
+            i += need[b]
+    kc, ks = R.cache(rng, pages, kv, page, D, spread)
+    vc, vs = R.cache(rng, pages, kv, page, D, spread)
+    q = torch.from_numpy(rng.standard_normal((int(cu[-1]) + pad, kv * G * D)).astype(np.float32)).to(q_dtype)
+    return q, cu, lens, table, kc, ks, vc, vs
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("B,kv,G,D,most,q_most", [(1, 1, 1, 64, 5, 1), (3, 2, 1, 128, 300, 1), (5, 2, 4, 64, 700, 2),
+                                                  (4, 1, 7, 128, 500, 3), (2, 3, 8, 128, 900, 8), (3, 1, 16, 256, 400, 5),
+                                                  (2, 2, 3, 256, 600, 1), (7, 2, 5, 128, 40, 6)])
+def test_attention_ragged(B, kv, G, D, most, q_most, page):
+    c = attn_case(B * 100 + D + page, B, kv, G, D, page, most, q_most, pad=2)
+    out, lse = attn_run(*c, D ** -0.5, q_most)
+    attn_check(out, lse, *c, D ** -0.5, q_most)
+
+
+@pytest.mark.parametrize("q_dtype,out_dtype", [(F32, F32), (BF, F32), (F32, BF)])
+def test_attention_types(q_dtype, out_dtype):
+    c = attn_case(7, 4, 2, 4, 128, 16, 500, 3, q_dtype=q_dtype)
+    out, lse = attn_run(*c, 0.09, 3, out_dtype=out_dtype)
+    attn_check(out, lse, *c, 0.09, 3)
+
+
+def test_attention_one_query_without_cu():
+    c = attn_case(8, 6, 2, 4, 64, 32, 300, 1, cu_given=False)
+    out, lse = attn_run(c[0], None, *c[2:], 0.125, 1)
+    attn_check(out, lse, *c, 0.125, 1)
+
+
+@pytest.mark.parametrize("G,q_most", [(4, 1), (3, 9), (8, 40)])
+def test_attention_long_sequences_are_split_and_joined(G, q_most):
+    """Many key blocks of few items, so that the runs' borders cut them; row tiles beyond one."""
+    rng = np.random.default_rng(9)
+    B, kv, D, page = 2, 1, 64, 64
+    lens = np.array([30011, 9000], np.int32)
+    n = np.array([q_most, 1])
+    cu = np.array([0, q_most, q_most + 1], np.int32)
+    need = (lens + page - 1) // page
+    pages = int(need.sum())
+    ids = rng.permutation(pages).astype(np.int32)
+    table = np.full((B, need.max()), -1, np.int32)
+    table[0, :need[0]], table[1, :need[1]] = ids[:need[0]], ids[need[0]:]
+    kc, ks = R.cache(rng, pages, kv, page, D)
+    vc, vs = R.cache(rng, pages, kv, page, D)
+    q = torch.from_numpy(rng.standard_normal((int(cu[-1]), G * D)).astype(np.float32)).to(BF)
+    c = (q, cu, lens, table, kc, ks, vc, vs)
+    out, lse = attn_run(*c, 0.125, q_most)
+    attn_check(out, lse, *c, 0.125, q_most)
+    again, lse2 = attn_run(*c, 0.125, q_most)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("spread", [0.0, 4.0, 12.0])
+def test_attention_page_scales_far_apart(spread):
+    """V pages whose scales differ by many powers of two (the accumulator changes its unit)."""
+    c = attn_case(10, 3, 2, 4, 128, 16, 400, 1, spread=spread)
+    out, lse = attn_run(*c, 0.01, 1)
+    attn_check(out, lse, *c, 0.01, 1)
+
+
+@pytest.mark.parametrize("low,high", [(0, 5), (0, 247), (27, 120), (20, 130)])
+def test_attention_smallest_and_largest_page_scales(low, high):
+    """V pages at the ends of the scale's range beside each other, and alone (all-zero blocks have byte 0)."""
+    c = list(attn_case(20, 4, 1, 2, 64, 16, 200, 1, spread=0.0))
+    rng = np.random.default_rng(20)
+    c[7] = np.where(rng.random(c[7].shape) < 0.5, low, high).astype(np.uint8)
+    if low == 0 and high > 100:
+        c[6][c[7][:, 0] == 0] = 0
+    table, lens = c[3], c[2]
+    for b in range(2):  # two sequences of low pages only
+        ids = table[b, :(lens[b] + 15) // 16]
+        c[7][ids] = low
+    out, lse = attn_run(*c, 0.05, 1, out_dtype=F32)
+    attn_check(out, lse, *c, 0.05, 1)
+
+
+def test_attention_sharp_and_extreme_queries():
+    """Scores of hundreds (one token takes all), zero queries, tiny and huge rows."""
+    c = list(attn_case(11, 5, 1, 4, 64, 32, 300, 1, spread=0.0))
+    c[0][0] *= 40.0
+    c[0][1] = 0.0
+    c[0][2] *= 1e-30
+    out, lse = attn_run(*c, 0.125, 1)
+    attn_check(out, lse, *c, 0.125, 1)
+
+
+def test_attention_masks_leave_rows_empty():
+    """Empty sequences, fewer tokens than queries, unnamed pages, lengths behind the table, more queries than max_q_len."""
+    rng = np.random.default_rng(12)
+    page, kv, G, D = 16, 2, 2, 64
+    kc, ks = R.cache(rng, 8, kv, page, D)
+    vc, vs = R.cache(rng, 8, kv, page, D)
+    table = np.array([[0, 1, 2], [3, 4, 5], [-1, 6, 99], [7, 0, 1], [2, 3, 4]], np.int32)
+    lens = np.array([0, 2, 40, 70, 33], np.int32)
+    cu = np.array([0, 2, 6, 7, 9, 13], np.int32)
+    q = torch.from_numpy(rng.standard_normal((15, kv * G * D)).astype(np.float32)).to(BF)
+    for max_q in (4, 3):
+        c = (q, cu, lens, table, kc, ks, vc, vs)
+        out, lse = attn_run(*c, 0.125, max_q)
+        attn_check(out, lse, *c, 0.125, max_q)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("page", [16, 64])
+def test_attention_nan_does_not_pass_the_mask(page, D):
+    """NaN codes behind the sequence reach nothing; a NaN token reaches the queries that see it, in V only its
+    own head dims."""
+    rng = np.random.default_rng(13)
+    kv, G, L, n = 1, 4, 75, 4
+    pages = 8
+    kc, ks = R.cache(rng, pages, kv, page, D)
+    vc, vs = R.cache(rng, pages, kv, page, D)
+    table = np.arange(pages, dtype=np.int32)[None]
+    cu, lens = np.array([0, n], np.int32), np.array([L], np.int32)
+    q = torch.from_numpy(rng.standard_normal((n, kv * G * D)).astype(np.float32)).to(BF)
+    clean, _ = attn_run(q, cu, lens, table, kc, ks, vc, vs, 0.1, n)
+    kc2, vc2 = kc.copy(), vc.copy()
+    for t in range(L, pages * page):
+        kc2[t // page, 0, t % page] = 0x7F
+        vc2[t // page, 0, t % page] = 0xFF
+    out, _ = attn_run(q, cu, lens, table, kc2, ks, vc2, vs, 0.1, n)
+    assert torch.equal(out, clean)
+    t = L - 2  # seen by the last two queries
+    vc2[t // page, 0, t % page, 5] = 0x7F
+    vc2[t // page, 0, t % page, D - 1] = 0xFF
+    out, _ = attn_run(q, cu, lens, table, kc2, ks, vc2, vs, 0.1, n)
+    o = out.view(n, G, D)
+    assert o[2:, :, [5, D - 1]].isnan().all()
+    rest = [d for d in range(D) if d not in (5, D - 1)]
+    assert torch.equal(o[:2], clean.view(n, G, D)[:2]) and torch.equal(o[2:][..., rest], clean.view(n, G, D)[2:][..., rest])
+    kc2[t // page, 0, t % page, 9] = 0x7F
+    out, _ = attn_run(q, cu, lens, table, kc2, ks, vc2, vs, 0.1, n)
+    assert out[2:].isnan().all() and torch.equal(out[:2], clean[:2])
+    vc2[0, 0, 3, 7] = 0x7F  # in a tile that every query sees whole
+    out, _ = attn_run(q, cu, lens, table, kc, ks, vc2, vs, 0.1, n)
+    assert out.view(n, G, D)[:, :, 7].isnan().all() and torch.equal(out.view(n, G, D)[:2, :, 8:], clean.view(n, G, D)[:2, :, 8:])
+
+
+def test_attention_strided_queries_and_outputs():
+    c = attn_case(14, 3, 2, 2, 64, 16, 100, 2)
+    q = c[0]
+    row = q.shape[1]
+    big = torch.full((q.shape[0], row + 128), float("nan"), dtype=BF, device="cuda")
+    big[:, 64:64 + row] = q.cuda()
+    out = torch.full((q.shape[0], row + 16), 7.0, dtype=BF, device="cuda")
+    ws = torch.empty(BQ.batq_attn_kv8_workspace_size(2, 4, 2, 64), dtype=torch.uint8, device="cuda")
+    BQ.batq_attn_kv8(big[:, 64:64 + row], *[R.cuda(a) for a in c[1:]], 0.125, 2, ws, out[:, 8:8 + row])
+    ok()
+    attn_check(out[:, 8:8 + row], None, *c, 0.125, 2)
+    assert (out[:, :8] == 7).all() and (out[:, 8 + row:] == 7).all()
+
+
+# ------------------------------------------------------------------ experts
+
+def experts_case(seed, counts, N, M, first=0, tail=0):
+    rng = np.random.default_rng(seed)
+    E, T = len(counts), first + sum(counts) + tail
+    off = (first + np.concatenate([[0], np.cumsum(counts)])).astype(np.int32)
+    ac, al = R.random_weights(rng, T, N, "mxfp4")
+    wc, wl = zip(*(R.random_weights(rng, M, N, "mxfp4") for _ in range(E)))
+    return off, ac, al, np.stack(wc), np.stack(wl)
+
+
+def experts_run(off, ac, al, wc, wl, out_dtype=F32):
+    E, M = wc.shape[:2]
+    T, N = ac.shape[0], 2 * ac.shape[1]
+    ws = np.stack([R.tile_scales(wl[e]) for e in range(E)])
+    out = torch.full((T, M), 7.0, dtype=out_dtype, device="cuda")
+    BQ.batq_gemm_mxfp4_experts(R.cuda(ac), R.cuda(al), R.cuda(wc), R.cuda(ws), R.cuda(off), M, N, out)
+    ok()
+    return out
+
+
+def experts_check(out, off, ac, al, wc, wl):
+    T, N = ac.shape[0], 2 * ac.shape[1]
+    a = R.weights(ac, al, "mxfp4")
+    got, mine = host(out), np.zeros(T, bool)
+    off = np.maximum.accumulate(np.clip(off, 0, T))
+    for e in range(wc.shape[0]):
+        lo, hi = off[e], off[e + 1]
+        if hi <= lo:
+            continue
+        w = R.weights(wc[e], wl[e], "mxfp4")
+        ref, mag = a[lo:hi] @ w.T, np.abs(a[lo:hi]) @ np.abs(w).T
+        # exact products; one fp32 step (truncated) per 64 K and their alignment inside, and the output's rounding
+        tol = mag * (N / 64 + 4) * 2.0 ** -22 + np.abs(ref) * (2.0 ** -8 if out.dtype == BF else 2.0 ** -24)
+        err = np.abs(got[lo:hi] - ref)
+        assert (err <= tol).all(), (e, (err / np.maximum(tol, 1e-300)).max())
+        mine[lo:hi] = True
+    assert (got[~mine] == 7).all(), "rows of no expert were written"
+
+
+@pytest.mark.parametrize("out_dtype", [F32, BF])
+@pytest.mark.parametrize("counts,N,M,first,tail", [
+    ([1], 64, 16, 0, 0), ([3, 0, 5], 128, 48, 2, 3), ([1, 16, 17, 0, 31, 32, 33], 576, 272, 0, 1),
+    ([255, 256, 257, 300], 512, 128, 0, 0), ([700, 0, 1], 2112, 400, 5, 7), ([40] * 70, 1024, 256, 0, 0),
+    ([0, 0, 1000], 1088, 1040, 0, 0), ([129] * 3, 4096, 512, 0, 0),
+])
+def test_experts_shapes(counts, N, M, first, tail, out_dtype):
+    c = experts_case(len(counts) + N, counts, N, M, first, tail)
+    experts_check(experts_run(*c, out_dtype), *c)
+
+
+def test_experts_no_rows_and_bad_offsets():
+    """Nothing for any expert; offsets outside the rows are clamped, and none counts as less than one before it."""
+    off, ac, al, wc, wl = experts_case(3, [10, 10, 10, 10], 256, 64)
+    for o in ([5, 5, 5, 5, 5], [-4, 7, 30, 20, 500], [40, 30, 20, 10, 0]):
+        o = np.array(o, np.int32)
+        experts_check(experts_run(o, ac, al, wc, wl), o, ac, al, wc, wl)
+
+
+def test_experts_many_experts():
+    rng = np.random.default_rng(4)
+    c = experts_case(5, list(rng.integers(0, 4, 512)), 128, 32)
+    experts_check(experts_run(*c), *c)
+
+
+def test_experts_non_finite_scales_stay_in_their_row():
+    off, ac, al, wc, wl = experts_case(6, [20, 300], 512, 256)
+    clean = experts_run(off, ac, al, wc, wl)
+    al[7, 3], wl[1, 9, 2] = 255, 255
+    out = experts_run(off, ac, al, wc, wl)
+    assert out[7].isnan().all() and out[20:, 9].isnan().all()
+    keep_r = [r for r in range(320) if r != 7]
+    keep_c = [c for c in range(256) if c != 9]
+    assert torch.equal(out[keep_r][:, keep_c], clean[keep_r][:, keep_c])
+
+
+def test_linear_experts_equals_its_two_halves():
+    rng = np.random.default_rng(7)
+    off, _, _, wc, wl = experts_case(7, [33, 0, 70, 5], 512, 128)
+    T, N, M = 108, 512, 128
+    X = torch.from_numpy(rng.standard_normal((T, N)).astype(np.float32)).to(BF).cuda()
+    A = (np.eye(8) + 0.1 * rng.standard_normal((8, 8))).astype(np.float32)
+    B = R.cuda((np.eye(4) + 0.1 * rng.standard_normal((N // 32, 4, 4))).astype(np.float32))
+    ratios = torch.full((N // 32 * 2,), 0.95, device="cuda")
+    w, s, o = R.cuda(wc), R.cuda(np.stack([R.tile_scales(x) for x in wl])), R.cuda(off)
+    out, ref = torch.empty(T, M, device="cuda"), torch.empty(T, M, device="cuda")
+    ws = torch.empty(BQ.batq_linear_experts_workspace_size(T, N), dtype=torch.uint8, device="cuda")
+    BQ.batq_linear_experts(X, A, B, ratios, w, s, o, M, ws, out)
+    codes, scales = BQ.empty_act_buffers(T, N, BQ.BATQ_SCALES_LINEAR)
+    BQ.batq_quant_act(X, A, B, ratios, codes, scales, BQ.BATQ_SCALES_LINEAR)
+    BQ.batq_gemm_mxfp4_experts(codes, scales, w, s, o, M, N, ref)
+    ok()
+    assert torch.equal(out, ref)
+    experts_check(ref, off, codes.cpu().numpy(), scales.cpu().numpy().reshape(T, -1), wc, wl)
