@@ -41,9 +41,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // kD: head dim; kMT: 16-row tiles per warp; kRW: row warps; kKW: key groups.
-template <int kD_, int kMT_, int kRW_, int kKW_, int kStages_>
+// kCtas: CTAs per SM that registers and shared memory are laid out for.
+template <int kD_, int kMT_, int kRW_, int kKW_, int kStages_, int kCtas_>
 struct AttnCfg {
-  static constexpr int kD = kD_, kMT = kMT_, kRW = kRW_, kKW = kKW_, kStages = kStages_;
+  static constexpr int kD = kD_, kMT = kMT_, kRW = kRW_, kKW = kKW_, kStages = kStages_,
+                       kCtas = kCtas_;
   static constexpr int kRowsPerWarp = 16 * kMT;
   static constexpr int kRows = kRowsPerWarp * kRW;
   static constexpr int kThreads = 32 * kRW * kKW;
@@ -135,6 +137,12 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
       : "r"(w));
 }
 
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(lo), "f"(hi));
@@ -164,7 +172,7 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
 __device__ __forceinline__ uint32_t lds32(const uint8_t* p) { return *reinterpret_cast<const uint32_t*>(p); }
 
 template <class C>
-__global__ void __launch_bounds__(C::kThreads)
+__global__ void __launch_bounds__(C::kThreads, C::kCtas)
     k_attn_kv8(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const AttnArgs a,
                const int q_bf16) {
   constexpr int kD = C::kD, kMT = C::kMT, kKW = C::kKW, kRW = C::kRW, kStages = C::kStages, kRows = C::kRows;
@@ -478,7 +486,7 @@ __global__ void __launch_bounds__(C::kThreads)
         if (__any_sync(0xffffffffu, m_new[0] > m[mt][0] || m_new[1] > m[mt][1])) {
 #pragma unroll
           for (int i2 = 0; i2 < 2; ++i2) {
-            const float alpha = m_new[i2] > m[mt][i2] ? exp2f(m[mt][i2] - m_new[i2]) : 1.0f;
+            const float alpha = m_new[i2] > m[mt][i2] ? ex2(m[mt][i2] - m_new[i2]) : 1.0f;
             m[mt][i2] = m_new[i2];
             l[mt][i2] *= alpha;
 #pragma unroll
@@ -495,7 +503,7 @@ __global__ void __launch_bounds__(C::kThreads)
           for (int n = 0; n < 4; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float p = exp2f(s[mt][n][2 * i2 + e] - base);
+              const float p = ex2(s[mt][n][2 * i2 + e] - base);
               s[mt][n][2 * i2 + e] = p;
               l[mt][i2] = fmaf(p, n < 2 ? vi0 : vi1, l[mt][i2]);
             }
@@ -844,12 +852,13 @@ cudaError_t launch_cfg(const AttnKv8Launch& L, cudaStream_t stream) {
 }
 
 // Rows of an item by the most rows a sequence can have (queries times heads per kv head).
-template <int kD, int kStages>
+template <int kD>
 cudaError_t launch_rows(const AttnKv8Launch& L, cudaStream_t stream) {
   const long long rows = (long long)L.max_q_len * (L.q_heads / L.kv_heads);
-  if (rows <= 16) return launch_cfg<AttnCfg<kD, 1, 1, 4, kStages>>(L, stream);
-  if (rows <= 32) return launch_cfg<AttnCfg<kD, 1, 2, 4, kStages>>(L, stream);
-  return launch_cfg<AttnCfg<kD, 1, 4, 2, kStages>>(L, stream);
+  constexpr bool kWide = kD == 256;  // two 16-row tiles per warp would not fit its registers
+  if (rows <= 16) return launch_cfg<AttnCfg<kD, 1, 1, 4, kD == 64 ? 4 : 2, kWide ? 1 : 3>>(L, stream);
+  if (rows <= 32) return launch_cfg<AttnCfg<kD, kWide ? 1 : 2, kWide ? 2 : 1, 4, kD == 64 ? 4 : 2, kWide ? 1 : 2>>(L, stream);
+  return launch_cfg<AttnCfg<kD, kWide ? 1 : 2, kWide ? 4 : 2, 2, kD == 64 ? 4 : 3, kWide ? 1 : 2>>(L, stream);
 }
 
 int rows_per_item(long long rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
@@ -863,9 +872,9 @@ size_t attn_kv8_workspace_bytes(int max_q_len, int q_heads, int kv_heads, int he
 
 cudaError_t launch_attn_kv8(const AttnKv8Launch& L, cudaStream_t stream) {
   switch (L.head_dim) {
-    case 64: return launch_rows<64, 4>(L, stream);
-    case 128: return launch_rows<128, 3>(L, stream);
-    case 256: return launch_rows<256, 2>(L, stream);
+    case 64: return launch_rows<64>(L, stream);
+    case 128: return launch_rows<128>(L, stream);
+    case 256: return launch_rows<256>(L, stream);
   }
   return cudaErrorInvalidValue;
 }

@@ -20,6 +20,7 @@
 // itself, across units, so the stream does not stop where a unit ends.  Partial sums are added over
 // the warps in shared memory, in order; when the tokens do not fit one CTA's shared memory, or when
 // there are few units, the CTAs of a cluster split K and add through distributed shared memory.
+#include <cmath>
 #include <cstdint>
 
 #include "host_util.h"
@@ -41,7 +42,7 @@ struct W4Args {
   const void* X;
   int x_bf16, S, N, ldx;
   int transform, split;       // split: y as two f16 columns
-  float A[64];
+  float A[64], a_norm;        // a_norm: largest column sum of |A|
   const float* B;
   const uint8_t* scales;
   const float* gs;
@@ -75,6 +76,17 @@ __device__ __forceinline__ void widen8(uint32_t w, uint32_t (&h)[4]) {
       : "r"(w));
 }
 
+// 2^(b - 127) of two E8M0 bytes, as the two bf16 halves of a word (exact; 255 gives NaN).
+__device__ __forceinline__ uint32_t e8m0x2(uint32_t bytes) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 h;\n\t"
+      "cvt.u16.u32 h, %1;\n\t"
+      "cvt.rn.bf16x2.ue8m0x2 %0, h;\n\t}"
+      : "=r"(r)
+      : "r"(bytes));
+  return r;
+}
+
 __device__ __forceinline__ uint16_t f16_bits(float v) {
   uint16_t r;
   asm("cvt.rn.f16.f32 %0, %1;" : "=h"(r) : "f"(v));
@@ -91,17 +103,28 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
   return v;
 }
 
-__device__ __forceinline__ float load_x(const W4Args& a, int s, int k) {
-  if (a.x_bf16)
-    return __uint_as_float((uint32_t) static_cast<const uint16_t*>(a.X)[(size_t)s * a.ldx + k] << 16);
-  return static_cast<const float*>(a.X)[(size_t)s * a.ldx + k];
+// Eight consecutive elements of token s.
+__device__ __forceinline__ void load_x8(const W4Args& a, int s, int k, float (&v)[8]) {
+  if (a.x_bf16) {
+    const uint4 q = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.X) + (size_t)s * a.ldx + k));
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  } else {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.X) + (size_t)s * a.ldx + k);
+    const float4 x = __ldg(p), y = __ldg(p + 1);
+    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+    v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+  }
 }
 
 // kNT: 8-column tiles of tokens.
 template <int kNT, bool kNv>
 __global__ void __launch_bounds__(kThreads)
     k_linear_w4a16(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ W4Args a) {
-  constexpr int kCols = 8 * kNT;
   constexpr int kTilesPerStage = kNv ? 4 : 2;     // scale tiles (four groups each) of a stage
   constexpr int kScaleBytes = kTilesPerStage * 128;
   extern __shared__ uint8_t smem_raw[];
@@ -112,11 +135,11 @@ __global__ void __launch_bounds__(kThreads)
   uint8_t* s_scales = smem + (size_t)kWarps * a.ring * kStageBytes + (size_t)warp * a.ring * kScaleBytes;
   uint8_t* s_x = smem + (size_t)kWarps * a.ring * (kStageBytes + kScaleBytes);
   const int cols = a.split ? 2 * a.S : a.S;
-  float* s_red = reinterpret_cast<float*>(s_x + (size_t)cols * a.x_pitch);  // [2][kWarps][kUnitRows][kCols]
-  float* s_a = s_red + 2 * kWarps * kUnitRows * kCols;                      // [64] A
-  float* s_xf = s_a + 64;                                                   // [16] 2^e of each token
+  float* s_red = reinterpret_cast<float*>(s_x + (size_t)cols * a.x_pitch);  // [2][kWarps][kUnitRows][16]
+  float* s_xf = s_red + 2 * kWarps * kUnitRows * kMaxW4A16Tokens;           // [16] 2^e of each token
   unsigned* s_amax = reinterpret_cast<unsigned*>(s_xf + 16);                // [16]
-  uint64_t* full = reinterpret_cast<uint64_t*>(s_amax + 16) + warp * kMaxStages;
+  float* s_sums = reinterpret_cast<float*>(s_amax + 16);                    // [2][kUnitRows * 16]
+  uint64_t* full = reinterpret_cast<uint64_t*>(s_sums + 2 * kUnitRows * kMaxW4A16Tokens) + warp * kMaxStages;
 
   uint32_t csize, crank;
   asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(csize));
@@ -131,7 +154,6 @@ __global__ void __launch_bounds__(kThreads)
     for (int i = 0; i < a.ring; ++i) mbar_init(&full[i], 1);
     fence_barrier_init();
   }
-  if (tid < 64) s_a[tid] = a.A[tid];
   if (tid < 16) s_amax[tid] = 0u;
   __syncwarp();
   griddep_wait();
@@ -165,68 +187,109 @@ __global__ void __launch_bounds__(kThreads)
   for (int i = 0; i < a.ring; ++i) issue();
   __syncthreads();
 
-  // y of this CTA's K range, twice: the token's largest magnitude, then the normalised f16 columns.
-  // A thread takes column d of one 4 x 8 block: four sums over A's column, then four over B's.
-  const int blocks = (k1 - k0) >> 5;
-  for (int pass = 0; pass < 2; ++pass) {
-    for (int x = tid; x < a.S * blocks * 8; x += kThreads) {
-      const int d = x & 7, blk = (x >> 3) % blocks, s = (x >> 3) / blocks;
-      const int k = k0 + blk * 32;
-      float y[4];
-      if (a.transform) {
-        float u[4];
+  // y of this CTA's K range.  A thread makes row b (eight values) of one 4 x 8 block:
+  // u = column b of B^T against the block's four rows, y = u A (A from the parameter bank).  First the
+  // bound of each token's magnitudes that the normalisation needs, |y| <= max|x| * |B|_1 * |A|_1 over
+  // its blocks (at most a few powers of two above the largest, out of f16's 28 spare ones).
+  const int rows = ((k1 - k0) >> 5) * 4;  // of each token
+  for (int s = 0; s < a.S; ++s) {
+    float m = 0.0f;
+    for (int x0 = tid; x0 < rows; x0 += 4 * kThreads) {
+      float v[4][8];
+      float4 br[4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          u[r] = 0.0f;
-#pragma unroll
-          for (int c = 0; c < 8; ++c) u[r] = fmaf(load_x(a, s, k + r * 8 + c), s_a[c * 8 + d], u[r]);
+      for (int j = 0; j < 4; ++j) {  // four rows in flight
+        const int x = x0 + j * kThreads;
+        if (x < rows) {
+          load_x8(a, s, k0 + x * 8, v[j]);
+          if (a.transform) br[j] = __ldg(reinterpret_cast<const float4*>(a.B + (size_t)(k0 >> 3) * 4 + x * 4));
         }
-        const float* B = a.B + (size_t)(k >> 5) * 16;
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          y[b] = 0.0f;
-#pragma unroll
-          for (int r = 0; r < 4; ++r) y[b] = fmaf(__ldg(B + r * 4 + b), u[r], y[b]);
-        }
-      } else {
-#pragma unroll
-        for (int b = 0; b < 4; ++b) y[b] = load_x(a, s, k + b * 8 + d);
       }
-      if (pass == 0) {
-        float m = 0.0f;
 #pragma unroll
-        for (int b = 0; b < 4; ++b) m = fabsf(y[b]) <= 3.402823466e38f ? fmaxf(m, fabsf(y[b])) : m;
-        atomicMax(&s_amax[s], __float_as_uint(m));  // non-negative floats order like their bits
-      } else {
-        const int e = max((int)(s_amax[s] >> 23) - 127 - 14, -126);
-        const float f = e8m0_value((uint32_t)(127 - e));
+      for (int j = 0; j < 4; ++j) {
+        if (x0 + j * kThreads < rows) {
+          float mj = 0.0f;
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          // Position within the block's 32: a lane reads eight consecutive ones, its four of the first
-          // and its four of the second instruction.
-          const int kk = b * 8 + d;
-          const int at = kNv ? ((kk & 15) >> 2) * 8 + (kk >> 4) * 4 + (kk & 3) : kk;
-          const float v = y[b] * f;
-          const uint16_t hi = f16_bits(v);
-          uint8_t* dst = s_x + (size_t)(blk * 32 + at) * 2;
-          *reinterpret_cast<uint16_t*>(dst + (size_t)s * a.x_pitch) = hi;
-          if (a.split) {
-            const uint16_t lo = (hi & 0x7C00u) == 0x7C00u ? 0 : f16_bits(v - f16_value(hi));
-            *reinterpret_cast<uint16_t*>(dst + (size_t)(a.S + s) * a.x_pitch) = lo;
-          }
+          for (int i = 0; i < 8; ++i) mj = fabsf(v[j][i]) <= 3.402823466e38f ? fmaxf(mj, fabsf(v[j][i])) : mj;
+          // Row b of B bounds what x's row b adds to any y: max |B[b][.]| max |x| |A|_1, four rows together.
+          if (a.transform)
+            mj *= 4.0f * a.a_norm *
+                  fmaxf(fmaxf(fabsf(br[j].x), fabsf(br[j].y)), fmaxf(fabsf(br[j].z), fabsf(br[j].w)));
+          m = fmaxf(m, fminf(mj, 3.402823466e38f));
         }
       }
     }
-    __syncthreads();
+    const unsigned bits = __reduce_max_sync(0xffffffffu, __float_as_uint(m));  // non-negative: ordered like their bits
+    if (lane == 0) atomicMax(&s_amax[s], bits);
   }
-  if (tid < a.S) s_xf[tid] = e8m0_value((uint32_t)(127 + max((int)(s_amax[tid] >> 23) - 127 - 14, -126)));
+  __syncthreads();
+  if (tid < a.S) {
+    const int e = max((int)(s_amax[tid] >> 23) - 127 - 14, -126);  // the bound * 2^-e lies in [2^14, 2^15)
+    s_xf[tid] = e8m0_value((uint32_t)(127 + e));
+  }
+  for (int s = 0; s < a.S; ++s)
+  for (int x = tid; x < rows; x += kThreads) {
+    const int b = x & 3, blk = x >> 2;
+    const int k = k0 + blk * 32;
+    const float f = e8m0_value((uint32_t)(127 - max((int)(s_amax[s] >> 23) - 127 - 14, -126)));
+    float y[8];
+    if (a.transform) {
+      float u[8];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        float v[8];
+        load_x8(a, s, k + r * 8, v);
+        const float w = __ldg(a.B + (size_t)(k >> 5) * 16 + r * 4 + b);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) u[c] = r == 0 ? w * v[c] : fmaf(w, v[c], u[c]);
+      }
+#pragma unroll
+      for (int d = 0; d < 8; ++d) {
+        y[d] = u[0] * a.A[d];
+#pragma unroll
+        for (int c = 1; c < 8; ++c) y[d] = fmaf(u[c], a.A[c * 8 + d], y[d]);
+      }
+    } else {
+      load_x8(a, s, k + b * 8, y);
+    }
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float v0 = y[2 * i] * f, v1 = y[2 * i + 1] * f;
+      const uint16_t h0 = f16_bits(v0), h1 = f16_bits(v1);
+      hi[i] = (uint32_t)h0 | ((uint32_t)h1 << 16);
+      if (a.split) {
+        const uint16_t l0 = (h0 & 0x7C00u) == 0x7C00u ? 0 : f16_bits(v0 - f16_value(h0));
+        const uint16_t l1 = (h1 & 0x7C00u) == 0x7C00u ? 0 : f16_bits(v1 - f16_value(h1));
+        lo[i] = (uint32_t)l0 | ((uint32_t)l1 << 16);
+      }
+    }
+    // Places in the block's 64 bytes: a lane of the products reads 16, its four elements of the first
+    // instruction and its four of the second.
+    uint8_t* dst = s_x + (size_t)(a.split ? 2 * s : s) * a.x_pitch + blk * 64;
+    uint8_t* dlo = dst + a.x_pitch;  // columns 2 s and 2 s + 1: one lane's pair of accumulators
+    if constexpr (kNv) {
+      // elements 8 b ..: the groups' halves, quads 2 (b & 1) and the next, instruction b >> 1
+      const int at = (b & 1) * 32 + (b >> 1) * 8;
+      *reinterpret_cast<uint2*>(dst + at) = make_uint2(hi[0], hi[1]);
+      *reinterpret_cast<uint2*>(dst + at + 16) = make_uint2(hi[2], hi[3]);
+      if (a.split) {
+        *reinterpret_cast<uint2*>(dlo + at) = make_uint2(lo[0], lo[1]);
+        *reinterpret_cast<uint2*>(dlo + at + 16) = make_uint2(lo[2], lo[3]);
+      }
+    } else {
+      *reinterpret_cast<uint4*>(dst + b * 16) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      if (a.split) *reinterpret_cast<uint4*>(dlo + b * 16) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+  }
   __syncthreads();
 
   float alpha = 1.0f;
   if constexpr (kNv) alpha = a.gs != nullptr ? 1.0f / *a.gs : 1.0f;
   const uint8_t* xcol[kNT];
 #pragma unroll
-  for (int n = 0; n < kNT; ++n) xcol[n] = s_x + (size_t)((n * 8 + g) % cols) * a.x_pitch + t * 16;
+  for (int n = 0; n < kNT; ++n)  // columns behind the last repeat the first
+    xcol[n] = s_x + (size_t)(n * 8 + g < cols ? n * 8 + g : 0) * a.x_pitch + t * 16;
 
   int slot = 0, parity = 0;
   uint32_t phase = 0;
@@ -249,6 +312,7 @@ __global__ void __launch_bounds__(kThreads)
       const int nblk = min(8, (a.N >> 5) - stage * 8);
       const int xoff = (stage - st0) * (kStageK * 2);
       uint4 sc;
+      uint32_t scf[4];  // MXFP4: bf16 scales of two blocks of the four row quarters
 #pragma unroll
       for (int b = 0; b < 8; ++b) {
         if (b >= nblk) break;
@@ -256,6 +320,13 @@ __global__ void __launch_bounds__(kThreads)
           if (b % 2 == 0) sc = *reinterpret_cast<const uint4*>(scales + (b >> 1) * 128);
         } else {
           if (b % 4 == 0) sc = *reinterpret_cast<const uint4*>(scales + (b >> 2) * 128);
+          if (b % 2 == 0) {
+            const int sh = (b & 2) * 8;
+            scf[0] = e8m0x2(sc.x >> sh);
+            scf[1] = e8m0x2(sc.y >> sh);
+            scf[2] = e8m0x2(sc.z >> sh);
+            scf[3] = e8m0x2(sc.w >> sh);
+          }
         }
         uint4 xv[kNT];
 #pragma unroll
@@ -277,8 +348,8 @@ __global__ void __launch_bounds__(kThreads)
           uint32_t h0[4], h1[4];
           widen8(w0, h0);
           widen8(w1, h1);
-          const uint32_t sw0 = q == 0 ? sc.x : sc.z, sw1 = q == 0 ? sc.y : sc.w;
           if constexpr (kNv) {
+            const uint32_t sw0 = q == 0 ? sc.x : sc.z, sw1 = q == 0 ? sc.y : sc.w;
             const int sh = (b & 1) * 16;
             const float2 f0 = e4m3x2_values((sw0 >> sh) & 0xFFFFu), f1 = e4m3x2_values((sw1 >> sh) & 0xFFFFu);
 #pragma unroll
@@ -292,7 +363,8 @@ __global__ void __launch_bounds__(kThreads)
               acc[q][n][3] = fmaf(d1[3], f1.y, fmaf(d0[3], f1.x, acc[q][n][3]));
             }
           } else {
-            const float f0 = e8m0_value((sw0 >> ((b & 3) * 8)) & 255u), f1 = e8m0_value((sw1 >> ((b & 3) * 8)) & 255u);
+            const float f0 = __uint_as_float((b & 1) ? scf[2 * q] & 0xFFFF0000u : scf[2 * q] << 16);
+            const float f1 = __uint_as_float((b & 1) ? scf[2 * q + 1] & 0xFFFF0000u : scf[2 * q + 1] << 16);
 #pragma unroll
             for (int n = 0; n < kNT; ++n) {
               float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -314,52 +386,73 @@ __global__ void __launch_bounds__(kThreads)
       issue();
     }
 
-    // Partial sums, in true units: rows q * 8 + i (quarter q), columns.
-    float* red = s_red + (size_t)parity * kWarps * kUnitRows * kCols;
-    float* mine = red + warp * kUnitRows * kCols;
+    // Partial sums, in true units: rows q * 8 + i (quarter q), tokens.
+    float* red = s_red + (size_t)parity * kWarps * kUnitRows * kMaxW4A16Tokens;
+    float* mine = red + warp * kUnitRows * kMaxW4A16Tokens;
 #pragma unroll
     for (int q = 0; q < 2; ++q)
 #pragma unroll
       for (int n = 0; n < kNT; ++n) {
-        const int col = n * 8 + 2 * t;
-        const float x0 = s_xf[col % a.S], x1 = s_xf[(col + 1) % a.S];
-        *reinterpret_cast<float2*>(mine + ((2 * q) * 8 + g) * kCols + col) =
-            make_float2(acc[q][n][0] * x0, acc[q][n][1] * x1);
-        *reinterpret_cast<float2*>(mine + ((2 * q + 1) * 8 + g) * kCols + col) =
-            make_float2(acc[q][n][2] * x0, acc[q][n][3] * x1);
-      }
-    if (csize > 1) cluster_sync_all(); else __syncthreads();
-    const int outs = kUnitRows * a.S;
-    for (int x = tid * csize + crank; x < outs; x += kThreads * csize) {
-      const int r = x & 31, s = x >> 5;
-      const int m = (unit >> 2) * 128 + (r >> 3) * 32 + (unit & 3) * 8 + (r & 7);
-      if (m >= a.M) continue;
-      float sum = 0.0f;
-      for (uint32_t c = 0; c < csize; ++c) {
-        const uint32_t base = csize > 1 ? mapa_shared(smem_u32(red), c) : smem_u32(red);
-        for (int w = 0; w < kWarps; ++w) {
-          const uint32_t at = base + (uint32_t)((w * kUnitRows + r) * kCols + s) * 4;
-          float v = csize > 1 ? ld_cluster_f32(at) : red[(w * kUnitRows + r) * kCols + s];
-          if (a.split)
-            v += csize > 1 ? ld_cluster_f32(at + (uint32_t)a.S * 4) : red[(w * kUnitRows + r) * kCols + a.S + s];
-          sum += v;
+        float* lo = mine + ((2 * q) * 8 + g) * kMaxW4A16Tokens;
+        float* hi = lo + 8 * kMaxW4A16Tokens;
+        if (a.split) {
+          const int s = n * 4 + t;
+          const float f = s_xf[s];
+          lo[s] = (acc[q][n][0] + acc[q][n][1]) * f;
+          hi[s] = (acc[q][n][2] + acc[q][n][3]) * f;
+        } else if constexpr (kNT <= 2) {
+          const int s = n * 8 + 2 * t;
+          const float f0 = s_xf[s], f1 = s_xf[s + 1];
+          *reinterpret_cast<float2*>(lo + s) = make_float2(acc[q][n][0] * f0, acc[q][n][1] * f1);
+          *reinterpret_cast<float2*>(hi + s) = make_float2(acc[q][n][2] * f0, acc[q][n][3] * f1);
         }
       }
+    __syncthreads();
+    // Sums over the warps, in order; thread x has row x % 32 of token x / 32.
+    const int outs = kUnitRows * a.S;
+    auto store = [&](int x, float sum) {
+      const int r = x & 31, s = x >> 5;
+      const int m = (unit >> 2) * 128 + (r >> 3) * 32 + (unit & 3) * 8 + (r & 7);
+      if (m >= a.M) return;
       sum *= alpha;
       const size_t o = (size_t)s * a.ldo + m;
       if (a.out_bf16)
         static_cast<uint16_t*>(a.out)[o] = (uint16_t)pack_bf16x2(sum, 0.0f);
       else
         static_cast<float*>(a.out)[o] = sum;
+    };
+    float* sums = s_sums + parity * (kUnitRows * kMaxW4A16Tokens);
+    for (int x = tid; x < outs; x += kThreads) {
+      const float* src = red + (x & 31) * kMaxW4A16Tokens + (x >> 5);
+      float v[kWarps];
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) v[w] = src[w * kUnitRows * kMaxW4A16Tokens];
+      float sum = v[0];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) sum += v[w];
+      if (csize > 1) sums[x] = sum; else store(x, sum);
+    }
+    if (csize > 1) {
+      // Then over the CTAs of the cluster, in order, each taking a share of the outputs.
+      cluster_sync_all();
+      for (int x = tid * csize + crank; x < outs; x += kThreads * csize) {
+        float v[8];
+#pragma unroll
+        for (uint32_t c = 0; c < 8; ++c) v[c] = c < csize ? ld_cluster_f32(mapa_shared(smem_u32(sums + x), c)) : 0.0f;
+        float sum = v[0];
+#pragma unroll
+        for (int c = 1; c < 8; ++c) sum += v[c];
+        store(x, sum);
+      }
     }
   }
   if (csize > 1) cluster_sync_all();  // peers may still read this CTA's sums
 }
 
-template <int kNT, bool kNv>
+template <bool kNv>
 size_t fixed_smem(int ring) {
   const size_t scale = kNv ? 512 : 256;
-  return (size_t)kWarps * ring * (kStageBytes + scale) + 2 * kWarps * kUnitRows * 8 * kNT * 4 + (64 + 16 + 16) * 4 +
+  return (size_t)kWarps * ring * (kStageBytes + scale) + 2 * kWarps * kUnitRows * kMaxW4A16Tokens * 4 + (16 + 16 + 2 * kUnitRows * kMaxW4A16Tokens) * 4 +
          kWarps * kMaxStages * 8 + 1024;
 }
 
@@ -371,13 +464,13 @@ cudaError_t launch_cfg(const LinearW4A16Launch& L, W4Args& a, int cols, cudaStre
   // Cluster size: enough CTAs along K for the columns to fit beside a ring of two stages.
   int csize = 1;
   auto pitch = [&](int c) { return (a.stages + c - 1) / c * kStageK * 2 + 64; };
-  while (csize < 8 && fixed_smem<kNT, kNv>(2) + (size_t)cols * pitch(csize) > kSmemLimit) ++csize;
-  if (fixed_smem<kNT, kNv>(2) + (size_t)cols * pitch(csize) > kSmemLimit) return cudaErrorInvalidConfiguration;
+  while (csize < 8 && fixed_smem<kNv>(2) + (size_t)cols * pitch(csize) > kSmemLimit) ++csize;
+  if (fixed_smem<kNv>(2) + (size_t)cols * pitch(csize) > kSmemLimit) return cudaErrorInvalidConfiguration;
   a.x_pitch = pitch(csize);
   const size_t xb = (size_t)cols * a.x_pitch;
   a.ring = 2;
-  while (a.ring < kMaxStages && fixed_smem<kNT, kNv>(a.ring + 1) + xb <= kSmemPair) ++a.ring;
-  const size_t smem = fixed_smem<kNT, kNv>(a.ring) + xb;
+  while (a.ring < kMaxStages && fixed_smem<kNv>(a.ring + 1) + xb <= kSmemPair) ++a.ring;
+  const size_t smem = fixed_smem<kNv>(a.ring) + xb;
   const int per_sm = smem <= kSmemPair ? 2 : 1;
 
   CUtensorMap tm;
@@ -393,11 +486,7 @@ cudaError_t launch_cfg(const LinearW4A16Launch& L, W4Args& a, int cols, cudaStre
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
-  int clusters = sm_count() * per_sm / csize;
-  if (clusters > a.units) clusters = a.units;
-  if (clusters < 1) clusters = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(clusters * csize));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -410,6 +499,23 @@ cudaError_t launch_cfg(const LinearW4A16Launch& L, W4Args& a, int cols, cudaStre
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
+  // As many clusters as run at the same time (clusters do not cross GPCs, so fewer than SMs / size).
+  int clusters = sm_count() * per_sm;
+  if (csize > 1) {
+    static int active[64][9] = {};
+    if (active[dev][csize] == 0) {
+      cfg.gridDim = dim3((unsigned)csize);
+      cudaLaunchConfig_t one = cfg;
+      one.dynamicSmemBytes = kSmemLimit;
+      int n = 0;
+      cudaError_t e = cudaOccupancyMaxActiveClusters(&n, kern, &one);
+      if (e != cudaSuccess) return e;
+      active[dev][csize] = n < 1 ? 1 : n;
+    }
+    clusters = active[dev][csize] * per_sm;
+  }
+  if (clusters > a.units) clusters = a.units;
+  cfg.gridDim = dim3((unsigned)(clusters * csize));
   return cudaLaunchKernelEx(&cfg, kern, tm, a);
 }
 
@@ -422,6 +528,11 @@ cudaError_t launch_fmt(const LinearW4A16Launch& L, cudaStream_t stream) {
   a.transform = L.transform;
   a.split = (L.transform || !L.x_bf16) ? 1 : 0;
   for (int i = 0; i < 64; ++i) a.A[i] = L.A[i];
+  for (int d = 0; d < 8; ++d) {
+    float sum = 0.0f;
+    for (int c = 0; c < 8; ++c) sum += std::fabs(L.A[c * 8 + d]);
+    a.a_norm = sum > a.a_norm ? sum : a.a_norm;
+  }
   a.B = L.B;
   a.scales = L.w_scales;
   a.gs = L.w_gs;
@@ -436,9 +547,7 @@ cudaError_t launch_fmt(const LinearW4A16Launch& L, cudaStream_t stream) {
   int per = L.S;
   auto fits = [&](int s) {
     const int cols = a.split ? 2 * s : s;
-    const int nt = cols <= 8 ? 1 : cols <= 16 ? 2 : 4;
-    const size_t fixed = nt == 1 ? fixed_smem<1, kNv>(2) : nt == 2 ? fixed_smem<2, kNv>(2) : fixed_smem<4, kNv>(2);
-    return fixed + (size_t)cols * ((a.stages + 7) / 8 * kStageK * 2 + 64) <= kSmemLimit;
+    return fixed_smem<kNv>(2) + (size_t)cols * ((a.stages + 7) / 8 * kStageK * 2 + 64) <= kSmemLimit;
   };
   while (per > 1 && !fits(per)) per = (per + 1) / 2;
   for (int s0 = 0; s0 < L.S; s0 += per) {
