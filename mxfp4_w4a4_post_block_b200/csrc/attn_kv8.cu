@@ -59,7 +59,7 @@ struct AttnCfg {
   static constexpr int kMergeBytes = kKW * kRows * kPitch * 4;
   static constexpr int kDataBytes = kRingBytes > kMergeBytes ? kRingBytes : kMergeBytes;  // the merge reuses the ring
   static constexpr int kQBytes = kRows * kD * 2;
-  static constexpr int kSmallBytes = kRows * 4 + 2 * kKW * kRows * 4 + 2 * kKW * kStages * 8 + kKW * kStages * 8 + 64;
+  static constexpr int kSmallBytes = kRows * 4 + 2 * kKW * kRows * 4 + 2 * kKW * kStages * 8 + kKW * kStages * 32 + 64;
   static constexpr int kSmemBytes = kDataBytes + kQBytes + kSmallBytes + 1024;
 };
 
@@ -149,6 +149,13 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
+// Maximum of three; NaN is passed over.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // V's page scales ride on the scores: with x_t the score in log2 units and 2^ev(t) the scale of token
 // t's V block, the weights in the matrix instruction are p_t = 2^(x_t + ev(t) - m + kBias), m the
 // running maximum of x + ev, and the sum takes p_t 2^-(ev(t) + kBias) = 2^(x_t - m).  So f16 keeps 11
@@ -177,14 +184,15 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
                const int q_bf16) {
   constexpr int kD = C::kD, kMT = C::kMT, kKW = C::kKW, kRW = C::kRW, kStages = C::kStages, kRows = C::kRows;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // (an offset, so that the compiler still knows these for shared addresses)
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* s_q = smem + C::kDataBytes;                                       // Q fragments (f16)
   float* s_rf = reinterpret_cast<float*>(s_q + C::kQBytes);                  // [kRows] scale of each row's scores
   float* s_m = s_rf + kRows;                                                 // [kKW][kRows]
   float* s_l = s_m + kKW * kRows;                                            // [kKW][kRows]
   uint64_t* s_full = reinterpret_cast<uint64_t*>(s_l + kKW * kRows);         // [kKW][kStages]
   uint64_t* s_empty = s_full + kKW * kStages;                                // [kKW][kStages]
-  uint2* s_meta = reinterpret_cast<uint2*>(s_empty + kKW * kStages);         // [kKW][kStages] scales, valid halves
+  float4* s_meta = reinterpret_cast<float4*>(s_empty + kKW * kStages);       // [kKW][kStages][2], see fetch
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int kw = warp / kRW, rw = warp % kRW;
@@ -234,7 +242,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
   uint8_t* ring = smem + kw * (kStages * C::kStageBytes);
   uint64_t* full = s_full + kw * kStages;
   uint64_t* empty = s_empty + kw * kStages;
-  uint2* meta = s_meta + kw * kStages;
+  float4* meta = s_meta + kw * kStages * 2;
   int p_slot = 0, c_slot = 0;         // producer's and consumer's ring slots
   uint32_t p_phase = 0, c_phase = 0;
 
@@ -260,66 +268,65 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
     const int my_tiles = tiles > kw ? (tiles - kw + kKW - 1) / kKW : 0;           // of this key group
 
     // ---------------------------------------------------------------- loads
-    // Lane l of the group's first warp holds what tile `batch0 + l` of the group needs.
-    int ids0 = -1, ids1 = -1, batch0 = 0;
-    uint32_t sc0 = 0, sc1 = 0;  // K scale | V scale << 8 of the first and second 16 keys
-    auto fetch_ids = [&](int i0) {
+    // Lane l of the group's first warp holds what tile `batch0 + l` of the group needs, and issues it:
+    // the rows of its pages in the cache's row list (-1: not named), and for each half of 16 keys the
+    // factors of the softmax: K's scale, V's exponent, and the sum's factor 2^-(exponent + bias).
+    int y0 = -1, y1 = -1, vb0 = 0, vb1 = 0, batch0 = 0;
+    float ks0, ks1, ev0, ev1;
+    const bool two = a.page_size == 16;  // a tile is two pages
+    auto fetch = [&](int i0) {
       batch0 = i0;
       const int key = key0 + ((i0 + lane) * kKW + kw) * kTile;
-      ids0 = ids1 = -1;
-      sc0 = sc1 = 0;
+      const int* row = a.page_table + (size_t)b * a.max_pages;
+      auto page = [&](int at, float& ks, float& ev, int& vb) {
+        ks = ev = 0.0f;
+        const int id = row[at];
+        if (id < 0 || id >= a.num_pages) return -1;
+        const int block = id * a.kv_heads + h;
+        ks = e8m0_value(a.k_scales[block]);
+        vb = a.v_scales[block];
+        ev = v_exponent(vb);
+        return block * a.page_size;
+      };
+      y0 = y1 = -1;
+      ks0 = ks1 = ev0 = ev1 = 0.0f;
       if (key < key_end) {
-        const int* row = a.page_table + (size_t)b * a.max_pages;
-        ids0 = row[key >> a.page_shift];
-        if (ids0 < 0 || ids0 >= a.num_pages) ids0 = -1;
-        ids1 = ids0;
-        if (a.page_size == 16) {
-          ids1 = key + 16 < key_end ? row[(key >> 4) + 1] : -1;
-          if (ids1 < 0 || ids1 >= a.num_pages) ids1 = -1;
-        }
-        if (ids0 >= 0) {
-          const size_t at = (size_t)ids0 * a.kv_heads + h;
-          sc0 = a.k_scales[at] | ((uint32_t)a.v_scales[at] << 8);
-        }
-        if (ids1 >= 0) {
-          const size_t at = (size_t)ids1 * a.kv_heads + h;
-          sc1 = a.k_scales[at] | ((uint32_t)a.v_scales[at] << 8);
-        }
+        y0 = page(key >> a.page_shift, ks0, ev0, vb0);
+        y1 = y0;
+        ks1 = ks0;
+        ev1 = ev0;
+        vb1 = vb0;
+        if (two) y1 = key + 16 < key_end ? page((key >> 4) + 1, ks1, ev1, vb1) : -1;
+        else if (y0 >= 0) y0 += key & (a.page_size - 1);
       }
     };
     // Issue tile i of the group into ring slot p_slot (whole warp; false on a timeout).
     auto issue = [&](int i) {
-      if (i - batch0 >= 32) fetch_ids(i);
-      const int src = i - batch0;
-      const int id0 = __shfl_sync(0xffffffffu, ids0, src), id1 = __shfl_sync(0xffffffffu, ids1, src);
-      const uint32_t m0 = __shfl_sync(0xffffffffu, sc0, src), m1 = __shfl_sync(0xffffffffu, sc1, src);
-      const bool ok = mbar_wait_warp(&empty[p_slot], p_phase ^ 1);
-      if (!ok) {
-        if (lane == 0) set_error(a.err, kErrReleaseTimeout);
-        return false;
+      if (i - batch0 >= 32) fetch(i);
+      if constexpr (kRW > 1) {  // with one warp per group the reader itself frees the slot
+        if (!mbar_wait_warp(&empty[p_slot], p_phase ^ 1)) {
+          if (lane == 0) set_error(a.err, kErrReleaseTimeout);
+          return false;
+        }
       }
-      if (lane == 0) {
-        const int key = key0 + (i * kKW + kw) * kTile;
-        meta[p_slot] = make_uint2(m0 | (m1 << 16), (id0 >= 0 ? 1u : 0u) | (id1 >= 0 ? 2u : 0u));
+      if (lane == i - batch0) {
+        meta[2 * p_slot] = make_float4(ks0, ev0, exp2f(-(float)kBias - ev0), __int_as_float((y0 >= 0) | (y1 >= 0) << 1));
+        meta[2 * p_slot + 1] = make_float4(ks1, ev1, exp2f(-(float)kBias - ev1), __int_as_float(vb0 | vb1 << 8));
+        uint64_t* bar = &full[p_slot];
         uint8_t* kdst = ring + p_slot * C::kStageBytes;
-        uint8_t* vdst = kdst + C::kTileBytes;
-        const bool two = a.page_size == 16;  // a tile is two 16-token pages
-        const int box_rows = two ? 16 : kTile;
-        const int boxes = two ? (id0 >= 0) + (id1 >= 0) : (id0 >= 0);
-        mbar_arrive_expect_tx(&full[p_slot], (uint32_t)(2 * boxes * box_rows * kD));
+        const int boxes = two ? (y0 >= 0) + (y1 >= 0) : 2 * (y0 >= 0);  // of 16 rows
+        mbar_arrive_expect_tx(bar, (uint32_t)(2 * boxes * 16 * kD));
 #pragma unroll
         for (int half = 0; half < C::kHalves; ++half) {
           uint8_t* kd = kdst + half * (kTile * C::kBoxD);
-          uint8_t* vd = vdst + half * (kTile * C::kBoxD);
-          if (id0 >= 0) {
-            const int y = (id0 * a.kv_heads + h) * a.page_size + (two ? 0 : (key & (a.page_size - 1)));
-            tma_load_2d(kd, &tm_k, &full[p_slot], half * C::kBoxD, y);
-            tma_load_2d(vd, &tm_v, &full[p_slot], half * C::kBoxD, y);
+          uint8_t* vd = kd + C::kTileBytes;
+          if (y0 >= 0) {
+            tma_load_2d(kd, &tm_k, bar, half * C::kBoxD, y0);
+            tma_load_2d(vd, &tm_v, bar, half * C::kBoxD, y0);
           }
-          if (two && id1 >= 0) {
-            const int y = (id1 * a.kv_heads + h) * 16;
-            tma_load_2d(kd + 16 * C::kBoxD, &tm_k, &full[p_slot], half * C::kBoxD, y);
-            tma_load_2d(vd + 16 * C::kBoxD, &tm_v, &full[p_slot], half * C::kBoxD, y);
+          if (two && y1 >= 0) {
+            tma_load_2d(kd + 16 * C::kBoxD, &tm_k, bar, half * C::kBoxD, y1);
+            tma_load_2d(vd + 16 * C::kBoxD, &tm_v, bar, half * C::kBoxD, y1);
           }
         }
       }
@@ -333,7 +340,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
 
     bool ok = true;
     if (rw == 0) {
-      fetch_ids(0);
+      fetch(0);
       for (int i = 0; i < min(my_tiles, kStages) && ok; ++i) ok = issue(i);
     }
 
@@ -366,8 +373,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       const int e = max((int)(__float_as_uint(amax) >> 23) - 127 - 14, -126);  // amax * 2^-e in [2^14, 2^15)
-      const float f = e8m0_value((uint32_t)(127 - e));
-      if (lane == 0) s_rf[r] = a.scale_log2 * e8m0_value((uint32_t)(127 + e));
+      const float f = copysignf(e8m0_value((uint32_t)(127 - e)), a.scale_log2);  // the scores' factor stays positive
+      if (lane == 0) s_rf[r] = fabsf(a.scale_log2) * e8m0_value((uint32_t)(127 + e));
       uint16_t* dst = reinterpret_cast<uint16_t*>(s_q) + (size_t)(r >> 4) * (16 * kD);
       const int hi_row = (r >> 3) & 1, gg = r & 7;
 #pragma unroll
@@ -409,9 +416,10 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
       }
       const uint8_t* kt = ring + c_slot * C::kStageBytes;
       const uint8_t* vt = kt + C::kTileBytes;
-      const uint2 mm = meta[c_slot];
+      const float4 h0 = meta[2 * c_slot], h1 = meta[2 * c_slot + 1];
+      const uint32_t named = __float_as_uint(h0.w);
       const int key = key0 + (i * kKW + kw) * kTile;
-      const bool whole = key + kTile <= full_end && mm.y == 3u;  // nothing of the tile is masked
+      const bool whole = key + kTile <= full_end && named == 3u;  // nothing of the tile is masked
 
       // Scores: four 8-key columns.
       float s[kMT][4][4];
@@ -456,32 +464,30 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
       }
 
       // Softmax.  Keys of column n: key + 8 n + 2 t + {0, 1}; n < 2 belong to the tile's first half.
-      const float ks0 = e8m0_value(mm.x & 255), ks1 = e8m0_value((mm.x >> 16) & 255);
-      const int vb0 = (int)((mm.x >> 8) & 255), vb1 = (int)(mm.x >> 24);
-      const float ev0 = v_exponent(vb0), ev1 = v_exponent(vb1);
-      const float vi0 = exp2f(-(float)kBias - ev0), vi1 = exp2f(-(float)kBias - ev1);
+      // The maximum is taken of the raw scores, whose factor is positive.
 #pragma unroll
       for (int mt = 0; mt < kMT; ++mt) {
+        uint32_t masked[2] = {0u, 0u};
+        if (!whole) {
+#pragma unroll
+          for (int i2 = 0; i2 < 2; ++i2)
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (key + 8 * n + 2 * t + e >= lim[mt][i2] || !((named >> (n >> 1)) & 1u)) {
+                  masked[i2] |= 1u << (2 * n + e);
+                  s[mt][n][2 * i2 + e] = -INFINITY;
+                }
+        }
         float m_new[2];
 #pragma unroll
         for (int i2 = 0; i2 < 2; ++i2) {
-          const float f0 = rf[mt][i2] * ks0, f1 = rf[mt][i2] * ks1;
-          float mx = -INFINITY;
-#pragma unroll
-          for (int n = 0; n < 4; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float x = fmaf(s[mt][n][2 * i2 + e], n < 2 ? f0 : f1, n < 2 ? ev0 : ev1);
-              if (!whole) {
-                const bool seen = key + 8 * n + 2 * t + e < lim[mt][i2] && ((mm.y >> (n >> 1)) & 1u);
-                x = seen ? x : -INFINITY;
-              }
-              s[mt][n][2 * i2 + e] = x;
-              mx = fmaxf(mx, x);
-            }
+          float mx0 = max3(fmaxf(s[mt][0][2 * i2], s[mt][0][2 * i2 + 1]), s[mt][1][2 * i2], s[mt][1][2 * i2 + 1]);
+          float mx1 = max3(fmaxf(s[mt][2][2 * i2], s[mt][2][2 * i2 + 1]), s[mt][3][2 * i2], s[mt][3][2 * i2 + 1]);
+          float mx = fmaxf(fmaf(mx0, rf[mt][i2] * h0.x, h0.y), fmaf(mx1, rf[mt][i2] * h1.x, h1.y));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          m_new[i2] = fmaxf(m[mt][i2], mx);
+          m_new[i2] = max3(m[mt][i2], mx, __shfl_xor_sync(0xffffffffu, mx, 2));
         }
         if (__any_sync(0xffffffffu, m_new[0] > m[mt][0] || m_new[1] > m[mt][1])) {
 #pragma unroll
@@ -503,9 +509,11 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
           for (int n = 0; n < 4; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float p = ex2(s[mt][n][2 * i2 + e] - base);
+              const float4 hh = n < 2 ? h0 : h1;
+              float p = ex2(fmaf(s[mt][n][2 * i2 + e], rf[mt][i2] * hh.x, hh.y - base));
+              if (!whole && ((masked[i2] >> (2 * n + e)) & 1u)) p = 0.0f;
               s[mt][n][2 * i2 + e] = p;
-              l[mt][i2] = fmaf(p, n < 2 ? vi0 : vi1, l[mt][i2]);
+              l[mt][i2] = fmaf(p, hh.z, l[mt][i2]);
             }
         }
       }
@@ -513,9 +521,9 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
       // o += P V, 16 keys at a time.
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
-        if (!((mm.y >> ks) & 1u)) continue;
-        const int vb = ks == 0 ? vb0 : vb1;
-        if (vb - 127 < kMinExp) {
+        if (!((named >> ks) & 1u)) continue;
+        if ((ks == 0 ? h0.y : h1.y) == (float)kMinExp) {
+          const int vb = (__float_as_int(h1.w) >> (8 * ks)) & 255;
           const float f = e8m0_value((uint32_t)(vb - kMinExp));
 #pragma unroll
           for (int mt = 0; mt < kMT; ++mt)
@@ -709,15 +717,21 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
   }
 }
 
-// Joins the partials of the items cut by run borders, in key order.  One CTA per (row tile, kv head, sequence).
+// Joins the partials of the items cut by run borders, in key order.  One warp per row: a lane weighs
+// every 32nd partial, then the lanes take the head dims and add all partials in order.
+// blockIdx.x: kv head and group of kJoinRows rows of the item list; y: sequence.
+constexpr int kJoinRows = 4;
 template <class C>
-__global__ void __launch_bounds__(128) k_attn_kv8_join(const AttnArgs a) {
-  constexpr int kD = C::kD, kRows = C::kRows;
+__global__ void __launch_bounds__(32 * kJoinRows) k_attn_kv8_join(const AttnArgs a, const int groups) {
+  constexpr int kD = C::kD, kRows = C::kRows, kPer = kD / 32;
+  __shared__ float s_w[kJoinRows][64];
   griddep_wait();
   griddep_launch_dependents();
-  const int b = blockIdx.z, h = blockIdx.y, rt = blockIdx.x, lane = threadIdx.x & 31;
+  const int b = blockIdx.y, h = blockIdx.x / groups, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rr = (blockIdx.x % groups) * kJoinRows + warp;  // row of the (sequence, kv head)
   const Items it = items_of<C>(a, b);
-  if (rt >= it.row_tiles) return;
+  const int rt = rr / kRows, r = rr % kRows;
+  if (rr >= it.s.count * a.group) return;
   long long W = 0, base = 0;
   for (int q = lane; q < a.batch; q += 32) {
     const long long n = items_of<C>(a, q).units(a.kv_heads);
@@ -733,47 +747,64 @@ __global__ void __launch_bounds__(128) k_attn_kv8_join(const AttnArgs a) {
   const long long u0 = base + (long long)(h * it.row_tiles + rt) * it.key_blocks, u1 = u0 + it.key_blocks;
   // Run of unit u: the last r with W r / runs <= u.
   auto run_of = [&](long long u) {
-    int r = (int)((u * runs) / W);
-    while (W * (r + 1) / runs <= u) ++r;
-    while (W * r / runs > u) --r;
-    return r;
+    int q = (int)((u * runs) / W);
+    while (W * (q + 1) / runs <= u) ++q;
+    while (W * q / runs > u) --q;
+    return q;
   };
   const int r0 = run_of(u0), r1 = run_of(u1 - 1);
   if (r0 == r1) return;  // written by its CTA
   const int slot0 = 2 * r0 + (W * r0 / runs == u0 ? 0 : 1);
   const float* ml = a.partial + (size_t)2 * a.runs * kRows * kD;
   const float* ll = ml + (size_t)2 * a.runs * kRows;
-  const int rows_here = min(kRows, it.s.count * a.group - rt * kRows);
-  constexpr int kQuads = kD / 4;
-  for (int x = threadIdx.x; x < rows_here * kQuads; x += 128) {
-    const int r = x / kQuads, d = (x % kQuads) * 4;
-    float mx = -INFINITY;
-    for (int c = r0; c <= r1; ++c) mx = fmaxf(mx, ml[(size_t)(c == r0 ? slot0 : 2 * c) * kRows + r]);
-    float sum = 0.0f;
-    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int c = r0; c <= r1; ++c) {
-      const size_t at = (size_t)(c == r0 ? slot0 : 2 * c) * kRows + r;
-      const float w = mx == -INFINITY ? 1.0f : exp2f(ml[at] - mx);
-      const float4 v = *reinterpret_cast<const float4*>(a.partial + at * kD + d);
-      sum += w * ll[at];
-      acc.x += w * v.x;
-      acc.y += w * v.y;
-      acc.z += w * v.z;
-      acc.w += w * v.w;
+  auto at = [&](int c) { return (size_t)(c == r0 ? slot0 : 2 * c) * kRows + r; };
+  float mx = -INFINITY;
+  for (int c = r0 + lane; c <= r1; c += 32) mx = fmaxf(mx, ml[at(c)]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  float sum = 0.0f, acc[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) acc[i] = 0.0f;
+  for (int c0 = r0; c0 <= r1; c0 += 64) {
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int c = c0 + 32 * j + lane;
+      float w = 0.0f;
+      if (c <= r1) {
+        w = mx == -INFINITY ? 1.0f : exp2f(ml[at(c)] - mx);
+        sum += w * ll[at(c)];
+      }
+      s_w[warp][32 * j + lane] = w;
     }
-    const float inv = sum == 0.0f ? 0.0f : kUnbias / sum;  // a row that sees nothing: zeros
-    const int rr = rt * kRows + r;
-    const size_t row = (size_t)(it.s.begin + rr / a.group);
-    const int head = h * a.group + rr % a.group;
-    const size_t at = row * (size_t)a.ldo + (size_t)head * kD + d;
-    if (a.out_bf16)
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
-          make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-    else
-      *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) =
-          make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-    if (a.lse && d == 0) a.lse[row * a.q_heads + head] = sum == 0.0f ? -INFINITY : kLn2 * (mx + log2f(sum));
+    __syncwarp();
+    const int n = min(64, r1 - c0 + 1);
+#pragma unroll 8
+    for (int c = 0; c < n; ++c) {
+      const float w = s_w[warp][c];
+      const float* src = a.partial + at(c0 + c) * kD + lane * kPer;
+#pragma unroll
+      for (int i = 0; i < kPer; i += 2) {
+        const float2 v = *reinterpret_cast<const float2*>(src + i);
+        acc[i] = fmaf(w, v.x, acc[i]);
+        acc[i + 1] = fmaf(w, v.y, acc[i + 1]);
+      }
+    }
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  const float inv = sum == 0.0f ? 0.0f : kUnbias / sum;  // a row that sees nothing: zeros
+  const size_t row = (size_t)(it.s.begin + rr / a.group);
+  const int head = h * a.group + rr % a.group;
+  const size_t o = row * (size_t)a.ldo + (size_t)head * kD + lane * kPer;
+#pragma unroll
+  for (int i = 0; i < kPer; i += 2) {
+    if (a.out_bf16)
+      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + o + i) = pack_bf16x2(acc[i] * inv, acc[i + 1] * inv);
+    else
+      *reinterpret_cast<float2*>(static_cast<float*>(a.out) + o + i) = make_float2(acc[i] * inv, acc[i + 1] * inv);
+  }
+  if (a.lse && lane == 0) a.lse[row * a.q_heads + head] = sum == 0.0f ? -INFINITY : kLn2 * (mx + log2f(sum));
 }
 
 constexpr int kMaxRuns = 444;  // 148 SMs x 3 CTAs
@@ -844,11 +875,12 @@ cudaError_t launch_cfg(const AttnKv8Launch& L, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   // No sequence can be longer than its page table: when that is one unit, no item is ever cut.
   if ((long long)L.max_pages * L.page_size <= C::kUnit) return cudaSuccess;
-  const int row_tiles = (int)(((long long)L.max_q_len * a.group + C::kRows - 1) / C::kRows);
-  cfg.gridDim = dim3((unsigned)row_tiles, (unsigned)L.kv_heads, (unsigned)L.batch);
-  cfg.blockDim = dim3(128);
+  const long long groups = ((long long)L.max_q_len * a.group + kJoinRows - 1) / kJoinRows;
+  if (groups * L.kv_heads >= (1LL << 31)) return cudaErrorInvalidConfiguration;
+  cfg.gridDim = dim3((unsigned)(groups * L.kv_heads), (unsigned)L.batch);
+  cfg.blockDim = dim3(32 * kJoinRows);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, k_attn_kv8_join<C>, a);
+  return cudaLaunchKernelEx(&cfg, k_attn_kv8_join<C>, a, (int)groups);
 }
 
 // Rows of an item by the most rows a sequence can have (queries times heads per kv head).

@@ -131,7 +131,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                    const __grid_constant__ CUtensorMap tm_x8, const __grid_constant__ CUtensorMap tm_x32,
                    const ExpertsArgs a) {
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // (an offset, so that the compiler still knows these for shared addresses)
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   int* s_off = reinterpret_cast<int*>(smem + kStages * kStageBytes);  // [E] {first row, rows}
   int* s_unit = s_off + 2 * kMaxExperts;                              // [E + 1] first tile of each expert
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kBarOffset);

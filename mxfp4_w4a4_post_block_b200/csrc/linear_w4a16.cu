@@ -128,7 +128,8 @@ __global__ void __launch_bounds__(kThreads)
   constexpr int kTilesPerStage = kNv ? 4 : 2;     // scale tiles (four groups each) of a stage
   constexpr int kScaleBytes = kTilesPerStage * 128;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // (an offset, so that the compiler still knows these for shared addresses)
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
   uint8_t* s_codes = smem + (size_t)warp * a.ring * kStageBytes;
