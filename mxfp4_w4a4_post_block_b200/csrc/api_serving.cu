@@ -155,6 +155,10 @@ batq_status batq_attn_kv8(const void* Q, batq_dtype q_dtype, int T, int ldq, int
   st = check_kv8(T, kv_heads, head_dim, cu_q_dev, seq_lens_dev, page_table_dev, batch, max_pages, num_pages, page_size,
                  k_codes, k_scales, v_codes, v_scales);
   if (st != BATQ_OK) return st;
+  // Work units (blocks of 64 keys or more of 8 rows or more) stay inside 32-bit arithmetic.
+  if ((long long)batch * kv_heads * (((long long)max_q_len * (q_heads / kv_heads) + 7) / 8) >
+      (1LL << 31) / (((long long)max_pages * page_size + 63) / 64 + 1))
+    return BATQ_ERR_SHAPE;
   const long long row = (long long)q_heads * head_dim;
   st = check_rows(Q, q_dtype, row, ldq);
   if (st != BATQ_OK) return st;

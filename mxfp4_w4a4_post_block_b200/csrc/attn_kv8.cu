@@ -5,28 +5,30 @@
 //   s_t = scale * 2^ek(t) * <q, K_t>,  t <= L - n + i;   p = softmax(s);   o = sum_t p_t 2^ev(t) V_t
 // in one pass over the cache with a running maximum and sum (fp32) per row.
 //
-// The G heads of a kv head times the queries are the rows of m16n8k16 matrix instructions: rows and
-// not keys fill the 16-row side, since K's and V's bytes are what has to move (a decode step does
-// about 2 G operations per byte; the tensor pipe idles).  E4M3 widens exactly to f16, so K and V
-// enter as f16 codes and the page scales stay outside: 2^ek multiplies the fp32 scores, 2^ev the
-// probabilities (below).  Q is rounded to f16 after an exact power-of-two normalisation of its row
-// (bf16 queries keep all their bits down to 2^-28 of the row's largest; fp32 queries keep 11);
-// probabilities are rounded to f16 (2^-11 relative), less than the bf16 output's own step.
+// The G heads of a kv head times the queries are the 8 columns, and K's and V's own dimensions the 16
+// rows, of m16n8k16 matrix instructions (S^T = K Q^T, O^T = V^T P^T): a decode step has few rows, and
+// with those on the 16-row side half of every instruction and accumulator would be padding.  E4M3
+// widens exactly to f16, so K and V enter as f16 codes and the page scales stay outside: 2^ek
+// multiplies the fp32 scores, 2^ev rides on them (below).  Q is rounded to f16 after an exact
+// power-of-two normalisation of its row (bf16 queries keep all their bits down to 2^-28 of the row's
+// largest; fp32 queries keep 11); probabilities are rounded to f16 (2^-11 relative), less than the
+// bf16 output's own step.
 //
 // Layout in registers.  The reduction dimensions may be ordered freely, as long as both operands
 // agree, so a lane reads 16 consecutive bytes of a K row (one LDS.128 feeds four K steps) and, of V,
-// four bytes (head dims) of each of four keys, transposed by byte permutes into the f16 pairs
-// (two keys of one head dim) that the instruction wants; the output then has eight consecutive head
-// dims per lane.  Tiles of 32 keys come by TMA with the 128-byte (head dim 64: 64-byte) swizzle,
-// which makes both reads conflict-free.
+// four bytes (head dims) of each of four keys, transposed by byte permutes into the f16 pairs (two
+// keys of one head dim) that the instruction wants; movmatrix turns the probabilities from S^T's
+// accumulator layout into the second product's operand.  Tiles of 32 keys come by TMA with the
+// 128-byte (head dim 64: 64-byte) swizzle, which makes both reads conflict-free.
 //
 // Work split.  The keys of all (sequence, kv head, row tile) items are cut into blocks of kUnit keys;
 // the list of all blocks is dealt out in equal contiguous runs, one per CTA, computed by each CTA
 // from seq_lens.  A CTA whose run covers an item writes its output; items cut by run borders leave
 // (m, l, o) partials in the workspace (at most two per CTA: its first and its last item), joined in
 // key order by k_attn_kv8_join.  Within a CTA, kKW key groups take every kKW-th tile, each with a
-// ring of its own, and kRW warps of a group share its tiles for further rows.
+// ring of its own (K and V tiles in turn), and kRW warps of a group share its tiles for further rows.
 #include <cstdint>
+#include <type_traits>
 
 #include "host_util.h"
 #include "kernels.h"
@@ -40,26 +42,25 @@ constexpr int kTile = 32;  // keys per tile
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// kD: head dim; kMT: 16-row tiles per warp; kRW: row warps; kKW: key groups.
-// kCtas: CTAs per SM that registers and shared memory are laid out for.
-template <int kD_, int kMT_, int kRW_, int kKW_, int kStages_, int kCtas_>
+// kD: head dim; kNT: 8-row tiles per warp; kRW: row warps; kKW: key groups; kSlots: ring slots (a K or
+// a V tile each) per key group; kCtas: CTAs per SM that registers and shared memory are laid out for.
+template <int kD_, int kNT_, int kRW_, int kKW_, int kSlots_, int kCtas_>
 struct AttnCfg {
-  static constexpr int kD = kD_, kMT = kMT_, kRW = kRW_, kKW = kKW_, kStages = kStages_,
-                       kCtas = kCtas_;
-  static constexpr int kRowsPerWarp = 16 * kMT;
+  static constexpr int kD = kD_, kNT = kNT_, kRW = kRW_, kKW = kKW_, kSlots = kSlots_, kCtas = kCtas_;
+  static constexpr int kRowsPerWarp = 8 * kNT;
   static constexpr int kRows = kRowsPerWarp * kRW;
   static constexpr int kThreads = 32 * kRW * kKW;
   static constexpr int kUnit = kTile * kKW;                 // keys per work unit
   static constexpr int kBoxD = kD < 128 ? kD : 128;         // bytes per row of one swizzled box
   static constexpr int kHalves = kD / kBoxD;                // boxes along the head dim
   static constexpr int kTileBytes = kTile * kD;
-  static constexpr int kStageBytes = 2 * kTileBytes;        // K, V
-  static constexpr int kRingBytes = kKW * kStages * kStageBytes;
+  static constexpr int kRingBytes = kKW * kSlots * kTileBytes;
   static constexpr int kPitch = kD + 4;                     // floats per row of the merge buffer
   static constexpr int kMergeBytes = kKW * kRows * kPitch * 4;
   static constexpr int kDataBytes = kRingBytes > kMergeBytes ? kRingBytes : kMergeBytes;  // the merge reuses the ring
+  static constexpr int kMetas = kSlots <= 4 ? 4 : 8;         // more than the tiles whose factors are alive at a time
   static constexpr int kQBytes = kRows * kD * 2;
-  static constexpr int kSmallBytes = kRows * 4 + 2 * kKW * kRows * 4 + 2 * kKW * kStages * 8 + kKW * kStages * 32 + 64;
+  static constexpr int kSmallBytes = kRows * 4 + 2 * kKW * kRows * 4 + 2 * kKW * kSlots * 8 + kKW * kMetas * 32 + 64;
   static constexpr int kSmemBytes = kDataBytes + kQBytes + kSmallBytes + 1024;
 };
 
@@ -75,7 +76,6 @@ struct AttnArgs {
   float scale_log2;
   int max_q_len;
   int runs;            // CTAs of the main kernel
-  int min_units;       // shortest run worth a CTA of its own
   float* partial;      // [2 * runs][rows][D], then m and l: [2 * runs][rows] each
   int out_bf16;
   void* out;
@@ -89,7 +89,7 @@ struct Items {
   SeqRows s;       // count: the queries to compute
   int queries;     // all of the sequence's, which places them
   int row_tiles, key_blocks;
-  __device__ long long units(int kv_heads) const { return (long long)kv_heads * row_tiles * key_blocks; }
+  __device__ int units(int kv_heads) const { return kv_heads * row_tiles * key_blocks; }
 };
 template <class C>
 __device__ __forceinline__ Items items_of(const AttnArgs& a, int b) {
@@ -103,20 +103,34 @@ __device__ __forceinline__ Items items_of(const AttnArgs& a, int b) {
   return it;
 }
 
-// Runs: with W units in all and R runs in use, run r is units [W r / R, W (r + 1) / R).
-__device__ __forceinline__ int runs_used(long long W, int runs, int min_units) {
-  const long long most = (W + min_units - 1) / min_units;
-  return (int)(most < runs ? (most > 0 ? most : 1) : runs);
+// The W units of the list in R runs of W / R, the first W % R of them one longer.
+struct Runs {
+  int count, size, longer;
+  __device__ int begin(int r) const { return r * size + min(r, longer); }
+  // Run of unit u.
+  __device__ int of(int u) const {
+    const int head = longer * (size + 1);
+    return u < head ? u / (size + 1) : longer + (u - head) / size;
+  }
+};
+__device__ __forceinline__ Runs runs_of(int W, int runs) {
+  Runs r;
+  r.count = min(W, runs);
+  r.size = W / max(r.count, 1);
+  r.longer = W - r.size * r.count;
+  return r;
 }
 
-// Sum of all units, by one warp (every lane gets it).
+// Units in all, and those before sequence b, by one warp (every lane gets them).
 template <class C>
-__device__ __forceinline__ long long total_units(const AttnArgs& a, int lane) {
-  long long w = 0;
-  for (int b = lane; b < a.batch; b += 32) w += items_of<C>(a, b).units(a.kv_heads);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
-  return w;
+__device__ __forceinline__ int2 count_units(const AttnArgs& a, int b, int lane) {
+  int w = 0, before = 0;
+  for (int q = lane; q < a.batch; q += 32) {
+    const int n = items_of<C>(a, q).units(a.kv_heads);
+    w += n;
+    before += q < b ? n : 0;
+  }
+  return make_int2(__reduce_add_sync(0xffffffffu, w), __reduce_add_sync(0xffffffffu, before));
 }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -178,21 +192,28 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
 
 __device__ __forceinline__ uint32_t lds32(const uint8_t* p) { return *reinterpret_cast<const uint32_t*>(p); }
 
+// Transposes an 8 x 8 matrix of 16-bit values held one row per four lanes.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
 template <class C>
 __global__ void __launch_bounds__(C::kThreads, C::kCtas)
     k_attn_kv8(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const AttnArgs a,
                const int q_bf16) {
-  constexpr int kD = C::kD, kMT = C::kMT, kKW = C::kKW, kRW = C::kRW, kStages = C::kStages, kRows = C::kRows;
+  constexpr int kD = C::kD, kNT = C::kNT, kKW = C::kKW, kRW = C::kRW, kSlots = C::kSlots, kRows = C::kRows;
   extern __shared__ uint8_t smem_raw[];
   // (an offset, so that the compiler still knows these for shared addresses)
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* s_q = smem + C::kDataBytes;                                       // Q fragments (f16)
-  float* s_rf = reinterpret_cast<float*>(s_q + C::kQBytes);                  // [kRows] scale of each row's scores
+  float* s_rf = reinterpret_cast<float*>(s_q + C::kQBytes);                  // [kRows] factor of each row's scores
   float* s_m = s_rf + kRows;                                                 // [kKW][kRows]
   float* s_l = s_m + kKW * kRows;                                            // [kKW][kRows]
-  uint64_t* s_full = reinterpret_cast<uint64_t*>(s_l + kKW * kRows);         // [kKW][kStages]
-  uint64_t* s_empty = s_full + kKW * kStages;                                // [kKW][kStages]
-  float4* s_meta = reinterpret_cast<float4*>(s_empty + kKW * kStages);       // [kKW][kStages][2], see fetch
+  float4* s_meta = reinterpret_cast<float4*>(s_l + kKW * kRows);             // [kKW][kMetas][2], see fetch
+  uint64_t* s_full = reinterpret_cast<uint64_t*>(s_meta + kKW * C::kMetas * 2);  // [kKW][kSlots]
+  uint64_t* s_empty = s_full + kKW * kSlots;                                 // [kKW][kSlots]
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int kw = warp / kRW, rw = warp % kRW;
@@ -200,7 +221,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
   if (tid == 0) {
     tma_prefetch_map(&tm_k);
     tma_prefetch_map(&tm_v);
-    for (int i = 0; i < kKW * kStages; ++i) {
+    for (int i = 0; i < kKW * kSlots; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&s_empty[i], kRW);
     }
@@ -210,26 +231,23 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
   griddep_launch_dependents();
   __syncthreads();
 
-  const long long W = total_units<C>(a, lane);
-  const int runs = runs_used(W, a.runs, a.min_units);
-  if ((int)blockIdx.x >= runs || W == 0) return;
-  long long u = W * blockIdx.x / runs;
-  const long long u_end = W * (blockIdx.x + 1) / runs;
-  const long long u_begin = u;
+  const Runs runs = runs_of(count_units<C>(a, 0, lane).x, a.runs);
+  if ((int)blockIdx.x >= runs.count) return;
+  int u = runs.begin(blockIdx.x);
+  const int u_begin = u, u_end = runs.begin(blockIdx.x + 1);
 
   // The sequence of unit u: each warp scans the batch.
   int b = 0;
-  long long base = 0;  // units before sequence b
+  int base = 0;  // units before sequence b
   for (int b0 = 0; b0 < a.batch; b0 += 32) {
-    const long long n = b0 + lane < a.batch ? items_of<C>(a, b0 + lane).units(a.kv_heads) : 0;
-    long long incl = n;
+    const int n = b0 + lane < a.batch ? items_of<C>(a, b0 + lane).units(a.kv_heads) : 0;
+    int incl = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += v;
     }
-    const bool here = n > 0 && base + incl > u && base + incl - n <= u;
-    const unsigned hit = __ballot_sync(0xffffffffu, here);
+    const unsigned hit = __ballot_sync(0xffffffffu, n > 0 && base + incl > u);
     if (hit) {
       const int src = __ffs(hit) - 1;
       b = b0 + src;
@@ -239,10 +257,10 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
     base += __shfl_sync(0xffffffffu, incl, 31);
   }
 
-  uint8_t* ring = smem + kw * (kStages * C::kStageBytes);
-  uint64_t* full = s_full + kw * kStages;
-  uint64_t* empty = s_empty + kw * kStages;
-  float4* meta = s_meta + kw * kStages * 2;
+  uint8_t* ring = smem + kw * (kSlots * C::kTileBytes);
+  uint64_t* full = s_full + kw * kSlots;
+  uint64_t* empty = s_empty + kw * kSlots;
+  float4* meta = s_meta + kw * C::kMetas * 2;
   int p_slot = 0, c_slot = 0;         // producer's and consumer's ring slots
   uint32_t p_phase = 0, c_phase = 0;
 
@@ -252,11 +270,10 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
       base += it.units(a.kv_heads);
       it = items_of<C>(a, ++b);
     }
-    const long long in_seq = u - base;
-    const int kb0 = (int)(in_seq % it.key_blocks);
-    const int item = (int)(in_seq / it.key_blocks);  // kv head, row tile
+    const int item = (u - base) / it.key_blocks;     // kv head, row tile
+    const int kb0 = (u - base) - item * it.key_blocks;
     const int rt = item % it.row_tiles, h = item / it.row_tiles;
-    const int kb1 = (int)min((long long)it.key_blocks, kb0 + (u_end - u));
+    const int kb1 = min(it.key_blocks, kb0 + (u_end - u));
     const int rows_here = min(kRows, it.s.count * a.group - rt * kRows);
     const int lim0 = it.s.len - it.queries + 1;      // keys that query 0 sees
     const int qi_first = rt * kRows / a.group;
@@ -272,7 +289,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
     // the rows of its pages in the cache's row list (-1: not named), and for each half of 16 keys the
     // factors of the softmax: K's scale, V's exponent, and the sum's factor 2^-(exponent + bias).
     int y0 = -1, y1 = -1, vb0 = 0, vb1 = 0, batch0 = 0;
-    float ks0, ks1, ev0, ev1;
+    float4 f0, f1;
     const bool two = a.page_size == 16;  // a tile is two pages
     auto fetch = [&](int i0) {
       batch0 = i0;
@@ -289,7 +306,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
         return block * a.page_size;
       };
       y0 = y1 = -1;
-      ks0 = ks1 = ev0 = ev1 = 0.0f;
+      float ks0 = 0.0f, ks1 = 0.0f, ev0 = 0.0f, ev1 = 0.0f;
       if (key < key_end) {
         y0 = page(key >> a.page_shift, ks0, ev0, vb0);
         y1 = y0;
@@ -299,9 +316,12 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
         if (two) y1 = key + 16 < key_end ? page((key >> 4) + 1, ks1, ev1, vb1) : -1;
         else if (y0 >= 0) y0 += key & (a.page_size - 1);
       }
+      f0 = make_float4(ks0, ev0, exp2f(-(float)kBias - ev0), __int_as_float((y0 >= 0) | (y1 >= 0) << 1));
+      f1 = make_float4(ks1, ev1, exp2f(-(float)kBias - ev1), __int_as_float(vb0 | vb1 << 8));
     };
-    // Issue tile i of the group into ring slot p_slot (whole warp; false on a timeout).
-    auto issue = [&](int i) {
+    // Issue load j of the group (tile j / 2: K, then V) into ring slot p_slot (whole warp; false on a timeout).
+    auto issue = [&](int j) {
+      const int i = j >> 1;
       if (i - batch0 >= 32) fetch(i);
       if constexpr (kRW > 1) {  // with one warp per group the reader itself frees the slot
         if (!mbar_wait_warp(&empty[p_slot], p_phase ^ 1)) {
@@ -310,28 +330,24 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
         }
       }
       if (lane == i - batch0) {
-        meta[2 * p_slot] = make_float4(ks0, ev0, exp2f(-(float)kBias - ev0), __int_as_float((y0 >= 0) | (y1 >= 0) << 1));
-        meta[2 * p_slot + 1] = make_float4(ks1, ev1, exp2f(-(float)kBias - ev1), __int_as_float(vb0 | vb1 << 8));
         uint64_t* bar = &full[p_slot];
-        uint8_t* kdst = ring + p_slot * C::kStageBytes;
+        uint8_t* dst = ring + p_slot * C::kTileBytes;
+        const CUtensorMap* map = (j & 1) ? &tm_v : &tm_k;
+        if (!(j & 1)) {
+          meta[2 * (i % C::kMetas)] = f0;
+          meta[2 * (i % C::kMetas) + 1] = f1;
+        }
         const int boxes = two ? (y0 >= 0) + (y1 >= 0) : 2 * (y0 >= 0);  // of 16 rows
-        mbar_arrive_expect_tx(bar, (uint32_t)(2 * boxes * 16 * kD));
+        mbar_arrive_expect_tx(bar, (uint32_t)(boxes * 16 * kD));
 #pragma unroll
         for (int half = 0; half < C::kHalves; ++half) {
-          uint8_t* kd = kdst + half * (kTile * C::kBoxD);
-          uint8_t* vd = kd + C::kTileBytes;
-          if (y0 >= 0) {
-            tma_load_2d(kd, &tm_k, bar, half * C::kBoxD, y0);
-            tma_load_2d(vd, &tm_v, bar, half * C::kBoxD, y0);
-          }
-          if (two && y1 >= 0) {
-            tma_load_2d(kd + 16 * C::kBoxD, &tm_k, bar, half * C::kBoxD, y1);
-            tma_load_2d(vd + 16 * C::kBoxD, &tm_v, bar, half * C::kBoxD, y1);
-          }
+          uint8_t* d = dst + half * (kTile * C::kBoxD);
+          if (y0 >= 0) tma_load_2d(d, map, bar, half * C::kBoxD, y0);
+          if (two && y1 >= 0) tma_load_2d(d + 16 * C::kBoxD, map, bar, half * C::kBoxD, y1);
         }
       }
       __syncwarp();
-      if (++p_slot == kStages) {
+      if (++p_slot == kSlots) {
         p_slot = 0;
         p_phase ^= 1;
       }
@@ -339,15 +355,28 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
     };
 
     bool ok = true;
+    const int loads = 2 * my_tiles;
     if (rw == 0) {
       fetch(0);
-      for (int i = 0; i < min(my_tiles, kStages) && ok; ++i) ok = issue(i);
+      for (int j = 0; j < min(loads, kSlots) && ok; ++j) ok = issue(j);
     }
+    // The slot just read is free: load j + kSlots goes there.
+    auto release = [&](int j) {
+      __syncwarp();
+      if constexpr (kRW > 1) {
+        if (lane == 0) mbar_arrive(&empty[c_slot]);
+      }
+      if (++c_slot == kSlots) {
+        c_slot = 0;
+        c_phase ^= 1;
+      }
+      if (rw == 0 && j + kSlots < loads) ok = issue(j + kSlots);
+    };
 
     // ---------------------------------------------------------------- Q
     // Row r: query qi = r / G, head h * G + r % G.  Each row is scaled by a power of two so that its
     // largest magnitude lies in [2^14, 2^15), then rounded to f16 and stored in fragment order:
-    // per (16-row tile, step of 16 head dims) 32 lanes x {row g lo, row g + 8 lo, row g hi, row g + 8 hi}.
+    // per (8-row tile, step of 16 head dims) 32 lanes x {row g lo, row g hi}.
     for (int r = warp; r < kRows; r += C::kThreads / 32) {
       constexpr int kPer = kD / 32;
       float v[kPer];
@@ -358,11 +387,19 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
         const size_t row = (size_t)(it.s.begin + rr / a.group);
         const size_t at = row * (size_t)a.ldq + (size_t)(h * a.group + rr % a.group) * kD + lane * kPer;
 #pragma unroll
+        for (int i = 0; i < kPer; i += 2) {
+          if (q_bf16) {
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.Q) + at + i);
+            v[i] = __uint_as_float(w << 16);
+            v[i + 1] = __uint_as_float(w & 0xFFFF0000u);
+          } else {
+            const float2 w = *reinterpret_cast<const float2*>(static_cast<const float*>(a.Q) + at + i);
+            v[i] = w.x;
+            v[i + 1] = w.y;
+          }
+        }
+#pragma unroll
         for (int i = 0; i < kPer; ++i) {
-          if (q_bf16)
-            v[i] = __uint_as_float((uint32_t) static_cast<const uint16_t*>(a.Q)[at + i] << 16);
-          else
-            v[i] = static_cast<const float*>(a.Q)[at + i];
           const float m = fabsf(v[i]);
           amax = m <= 3.402823466e38f ? fmaxf(amax, m) : amax;
         }
@@ -370,302 +407,275 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
 #pragma unroll
         for (int i = 0; i < kPer; ++i) v[i] = 0.0f;
       }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));  // not negative: ordered as bits
       const int e = max((int)(__float_as_uint(amax) >> 23) - 127 - 14, -126);  // amax * 2^-e in [2^14, 2^15)
       const float f = copysignf(e8m0_value((uint32_t)(127 - e)), a.scale_log2);  // the scores' factor stays positive
       if (lane == 0) s_rf[r] = fabsf(a.scale_log2) * e8m0_value((uint32_t)(127 + e));
-      uint16_t* dst = reinterpret_cast<uint16_t*>(s_q) + (size_t)(r >> 4) * (16 * kD);
-      const int hi_row = (r >> 3) & 1, gg = r & 7;
+      uint8_t* dst = s_q + (size_t)(r >> 3) * (8 * kD * 2);
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        // head dim -> (16-byte chunk c of the K row, byte in it): lane (c >> 1) & 3 or c & 3, step, register.
+      for (int i = 0; i < kPer; i += 2) {
+        // head dim -> 16-byte chunk c of the K row and the byte in it: lane c >> 1 (c for 64-byte rows), step, register
         const int d = lane * kPer + i;
         const int half = d / C::kBoxD, c = (d % C::kBoxD) >> 4, within = d & 15;
         const int tt = C::kBoxD == 128 ? c >> 1 : c;
         const int step = (half * (C::kBoxD / 64) + (C::kBoxD == 128 ? (c & 1) : 0)) * 4 + (within >> 2);
-        const int reg = ((within >> 1) & 1) * 2 + hi_row;
-        const uint32_t pk = pack_f16x2(v[i] * f, 0.0f);
-        dst[(size_t)step * 256 + (gg * 4 + tt) * 8 + reg * 2 + (within & 1)] = (uint16_t)pk;
+        *reinterpret_cast<uint32_t*>(dst + step * 256 + ((r & 7) * 4 + tt) * 8 + ((within >> 1) & 1) * 4) =
+            pack_f16x2(v[i] * f, v[i + 1] * f);
       }
     }
     __syncthreads();
 
     // ---------------------------------------------------------------- tiles
-    float o[kMT][kD / 8][4];
-    float m[kMT][2], l[kMT][2], rf[kMT][2];
-    int lim[kMT][2];
+    // This lane's rows: 8 n + 2 t and the next of its warp's; keys of a tile: 16 mk + g and + 8.
+    float o[kD / 16][kNT][4];
+    float m[kNT][2], l[kNT][2], rf[kNT][2];
+    int lim[kNT][2];
 #pragma unroll
-    for (int mt = 0; mt < kMT; ++mt) {
+    for (int n = 0; n < kNT; ++n) {
 #pragma unroll
-      for (int n = 0; n < kD / 8; ++n) o[mt][n][0] = o[mt][n][1] = o[mt][n][2] = o[mt][n][3] = 0.0f;
+      for (int d = 0; d < kD / 16; ++d) o[d][n][0] = o[d][n][1] = o[d][n][2] = o[d][n][3] = 0.0f;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int r = rw * C::kRowsPerWarp + mt * 16 + g + 8 * i;
-        m[mt][i] = -INFINITY;
-        l[mt][i] = 0.0f;
-        rf[mt][i] = s_rf[r];
-        lim[mt][i] = min(lim0 + (rt * kRows + r) / a.group, it.s.len);
+        const int r = rw * C::kRowsPerWarp + n * 8 + 2 * t + i;
+        m[n][i] = -INFINITY;
+        l[n][i] = 0.0f;
+        rf[n][i] = s_rf[r];
+        lim[n][i] = min(lim0 + (rt * kRows + r) / a.group, it.s.len);
       }
     }
-    for (int i = 0; i < my_tiles && ok; ++i) {
-      if (!mbar_wait_warp(&full[c_slot], c_phase)) {
-        if (lane == 0) set_error(a.err, kErrDataTimeout);
-        ok = false;
-        break;
-      }
-      const uint8_t* kt = ring + c_slot * C::kStageBytes;
-      const uint8_t* vt = kt + C::kTileBytes;
-      const float4 h0 = meta[2 * c_slot], h1 = meta[2 * c_slot + 1];
-      const uint32_t named = __float_as_uint(h0.w);
-      const int key = key0 + (i * kKW + kw) * kTile;
-      const bool whole = key + kTile <= full_end && named == 3u;  // nothing of the tile is masked
+    // Places in a swizzled tile, head dim chunks XORed with the row: the 16 bytes (2 t; 64-byte rows: t) of
+    // key g, and the four bytes 4 g .. of keys 2 t and 2 t + 1.  Rows 8 further have the same pattern.
+    uint32_t k_at, v_at[2];
+    if constexpr (C::kBoxD == 128) {
+      k_at = g * 128 + (((2 * t) ^ g) << 4);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) v_at[q] = (2 * t + q) * 128 + (((g >> 2) ^ (2 * t + q)) << 4) + (g & 3) * 4;
+    } else {
+      k_at = g * 64 + ((t ^ ((g >> 1) & 3)) << 4);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) v_at[q] = (2 * t + q) * 64 + (((g >> 2) ^ t) << 4) + (g & 3) * 4;
+    }
+    const uint8_t* my_q = s_q + rw * (C::kRowsPerWarp * kD * 2) + lane * 8;
+    auto landed = [&]() {
+      if (mbar_wait_warp(&full[c_slot], c_phase)) return true;
+      if (lane == 0) set_error(a.err, kErrDataTimeout);
+      return ok = false;
+    };
+    // Tile i, whose K has landed.  kWhole: nothing of it is masked (all but a sequence's last tiles).
+    auto tile = [&](auto whole_tag, const int i, const int key, const float4 h0, const float4 h1) {
+      constexpr bool kWhole = decltype(whole_tag)::value;
+      const uint32_t named = kWhole ? 3u : __float_as_uint(h0.w);
 
-      // Scores: four 8-key columns.
-      float s[kMT][4][4];
+      // S^T: two 16-key tiles by the warp's rows.
+      float s[2][kNT][4];
 #pragma unroll
-      for (int mt = 0; mt < kMT; ++mt)
+      for (int n = 0; n < kNT; ++n)
 #pragma unroll
-        for (int n = 0; n < 4; ++n) s[mt][n][0] = s[mt][n][1] = s[mt][n][2] = s[mt][n][3] = 0.0f;
+        for (int mk = 0; mk < 2; ++mk) s[mk][n][0] = s[mk][n][1] = s[mk][n][2] = s[mk][n][3] = 0.0f;
+      {
+        const uint8_t* kt = ring + c_slot * C::kTileBytes;
 #pragma unroll
-      for (int c = 0; c < kD / 64; ++c) {  // 64 head dims: 16 bytes per lane
-        uint4 kq[4];
+        for (int c = 0; c < kD / 64; ++c) {  // 64 head dims: 16 bytes per lane and key
+          uint4 kq[4];
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          const int row = n * 8 + g;
-          if constexpr (C::kBoxD == 128) {
-            const int half = c >> 1, chunk = 2 * t + (c & 1);
-            kq[n] = *reinterpret_cast<const uint4*>(kt + half * (kTile * 128) + row * 128 + ((chunk ^ (row & 7)) << 4));
-          } else {
-            kq[n] = *reinterpret_cast<const uint4*>(kt + row * 64 + ((t ^ ((row >> 1) & 3)) << 4));
+          for (int n = 0; n < 4; ++n)
+            kq[n] = *reinterpret_cast<const uint4*>(kt + (k_at ^ ((c & 1) << 4)) + (c >> 1) * (kTile * 128) +
+                                                    n * (8 * C::kBoxD));
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint2 q[kNT];
+#pragma unroll
+            for (int n = 0; n < kNT; ++n)
+              q[n] = *reinterpret_cast<const uint2*>(my_q + n * (8 * kD * 2) + (c * 4 + j) * 256);
+#pragma unroll
+            for (int mk = 0; mk < 2; ++mk) {
+              uint32_t ka[4];
+              const uint4 k0 = kq[2 * mk], k1 = kq[2 * mk + 1];
+              widen4(j == 0 ? k0.x : j == 1 ? k0.y : j == 2 ? k0.z : k0.w, ka[0], ka[2]);
+              widen4(j == 0 ? k1.x : j == 1 ? k1.y : j == 2 ? k1.z : k1.w, ka[1], ka[3]);
+#pragma unroll
+              for (int n = 0; n < kNT; ++n) mma_f16(s[mk][n], ka, q[n].x, q[n].y);
+            }
           }
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t qa[kMT][4];
-#pragma unroll
-          for (int mt = 0; mt < kMT; ++mt) {
-            const uint4 q = *reinterpret_cast<const uint4*>(s_q + (size_t)(rw * kMT + mt) * (16 * kD * 2) +
-                                                            (c * 4 + j) * 512 + lane * 16);
-            qa[mt][0] = q.x;
-            qa[mt][1] = q.y;
-            qa[mt][2] = q.z;
-            qa[mt][3] = q.w;
-          }
-#pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            const uint32_t w = j == 0 ? kq[n].x : j == 1 ? kq[n].y : j == 2 ? kq[n].z : kq[n].w;
-            uint32_t b0, b1;
-            widen4(w, b0, b1);
-#pragma unroll
-            for (int mt = 0; mt < kMT; ++mt) mma_f16(s[mt][n], qa[mt], b0, b1);
-          }
-        }
       }
+      release(2 * i);
 
-      // Softmax.  Keys of column n: key + 8 n + 2 t + {0, 1}; n < 2 belong to the tile's first half.
-      // The maximum is taken of the raw scores, whose factor is positive.
+      // Softmax.  The maximum is taken of the raw scores, whose factor is positive.
+      uint32_t pb[2][kNT][2];  // P^T: the second product's operand
 #pragma unroll
-      for (int mt = 0; mt < kMT; ++mt) {
-        uint32_t masked[2] = {0u, 0u};
-        if (!whole) {
+      for (int n = 0; n < kNT; ++n) {
+        uint32_t masked = 0;
+        if constexpr (!kWhole) {
 #pragma unroll
-          for (int i2 = 0; i2 < 2; ++i2)
+          for (int mk = 0; mk < 2; ++mk)
 #pragma unroll
-            for (int n = 0; n < 4; ++n)
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-                if (key + 8 * n + 2 * t + e >= lim[mt][i2] || !((named >> (n >> 1)) & 1u)) {
-                  masked[i2] |= 1u << (2 * n + e);
-                  s[mt][n][2 * i2 + e] = -INFINITY;
-                }
+            for (int e = 0; e < 4; ++e)
+              if (key + 16 * mk + g + 8 * (e >> 1) >= lim[n][e & 1] || !((named >> mk) & 1u)) {
+                masked |= 1u << (4 * mk + e);
+                s[mk][n][e] = -INFINITY;
+              }
         }
         float m_new[2];
 #pragma unroll
-        for (int i2 = 0; i2 < 2; ++i2) {
-          float mx0 = max3(fmaxf(s[mt][0][2 * i2], s[mt][0][2 * i2 + 1]), s[mt][1][2 * i2], s[mt][1][2 * i2 + 1]);
-          float mx1 = max3(fmaxf(s[mt][2][2 * i2], s[mt][2][2 * i2 + 1]), s[mt][3][2 * i2], s[mt][3][2 * i2 + 1]);
-          float mx = fmaxf(fmaf(mx0, rf[mt][i2] * h0.x, h0.y), fmaf(mx1, rf[mt][i2] * h1.x, h1.y));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          m_new[i2] = max3(m[mt][i2], mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        for (int e = 0; e < 2; ++e) {
+          const float x0 = fmaf(fmaxf(s[0][n][e], s[0][n][2 + e]), rf[n][e] * h0.x, h0.y);
+          const float x1 = fmaf(fmaxf(s[1][n][e], s[1][n][2 + e]), rf[n][e] * h1.x, h1.y);
+          float mx = fmaxf(x0, x1);
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+          m_new[e] = max3(m[n][e], mx, __shfl_xor_sync(0xffffffffu, mx, 16));
         }
-        if (__any_sync(0xffffffffu, m_new[0] > m[mt][0] || m_new[1] > m[mt][1])) {
+        if (__any_sync(0xffffffffu, m_new[0] > m[n][0] || m_new[1] > m[n][1])) {
+          float alpha[2];
 #pragma unroll
-          for (int i2 = 0; i2 < 2; ++i2) {
-            const float alpha = m_new[i2] > m[mt][i2] ? ex2(m[mt][i2] - m_new[i2]) : 1.0f;
-            m[mt][i2] = m_new[i2];
-            l[mt][i2] *= alpha;
-#pragma unroll
-            for (int n = 0; n < kD / 8; ++n) {
-              o[mt][n][2 * i2] *= alpha;
-              o[mt][n][2 * i2 + 1] *= alpha;
-            }
+          for (int e = 0; e < 2; ++e) {
+            alpha[e] = m_new[e] > m[n][e] ? ex2(m[n][e] - m_new[e]) : 1.0f;
+            m[n][e] = m_new[e];
+            l[n][e] *= alpha[e];
           }
+#pragma unroll
+          for (int d = 0; d < kD / 16; ++d)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[d][n][e] *= alpha[e & 1];
+        }
+        float b0[2], b1[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float base_e = m[n][e] == -INFINITY ? 0.0f : m[n][e] - (float)kBias;
+          b0[e] = h0.y - base_e;
+          b1[e] = h1.y - base_e;
         }
 #pragma unroll
-        for (int i2 = 0; i2 < 2; ++i2) {
-          const float base = m[mt][i2] == -INFINITY ? 0.0f : m[mt][i2] - (float)kBias;
+        for (int mk = 0; mk < 2; ++mk) {
+          const float4 hh = mk == 0 ? h0 : h1;
+          float p[4];
 #pragma unroll
-          for (int n = 0; n < 4; ++n)
+          for (int e = 0; e < 4; ++e) {
+            p[e] = ex2(fmaf(s[mk][n][e], rf[n][e & 1] * hh.x, mk == 0 ? b0[e & 1] : b1[e & 1]));
+            if (!kWhole && ((masked >> (4 * mk + e)) & 1u)) p[e] = 0.0f;
+            l[n][e & 1] = fmaf(p[e], hh.z, l[n][e & 1]);
+          }
+          if (hh.y == (float)kMinExp) {
+            const float f = e8m0_value((uint32_t)(((__float_as_int(h1.w) >> (8 * mk)) & 255) - kMinExp));
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float4 hh = n < 2 ? h0 : h1;
-              float p = ex2(fmaf(s[mt][n][2 * i2 + e], rf[mt][i2] * hh.x, hh.y - base));
-              if (!whole && ((masked[i2] >> (2 * n + e)) & 1u)) p = 0.0f;
-              s[mt][n][2 * i2 + e] = p;
-              l[mt][i2] = fmaf(p, hh.z, l[mt][i2]);
-            }
+            for (int e = 0; e < 4; ++e) p[e] *= f;
+          }
+          pb[mk][n][0] = transpose8x8(pack_f16x2(p[0], p[1]));
+          pb[mk][n][1] = transpose8x8(pack_f16x2(p[2], p[3]));
         }
       }
 
-      // o += P V, 16 keys at a time.
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        if (!((named >> ks) & 1u)) continue;
-        if ((ks == 0 ? h0.y : h1.y) == (float)kMinExp) {
-          const int vb = (__float_as_int(h1.w) >> (8 * ks)) & 255;
-          const float f = e8m0_value((uint32_t)(vb - kMinExp));
-#pragma unroll
-          for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              s[mt][2 * ks][e] *= f;
-              s[mt][2 * ks + 1][e] *= f;
-            }
+      // O^T += V^T P^T, 16 keys at a time.
+      if (!landed()) return;
+      const uint8_t* vt = ring + c_slot * C::kTileBytes;
+      // Four head dims (4 g ..) of the 32-dim group dg of any key of this tile.
+      auto v_word = [&](int row, int dg) {
+        if constexpr (C::kBoxD == 128) {
+          const int half = dg >> 2, chunk = (dg & 3) * 2 + (g >> 2);
+          return lds32(vt + half * (kTile * 128) + row * 128 + ((chunk ^ (row & 7)) << 4) + (g & 3) * 4);
+        } else {
+          const int chunk = dg * 2 + (g >> 2);
+          return lds32(vt + row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4) + (g & 3) * 4);
         }
-        uint32_t pa[kMT][4];
+      };
 #pragma unroll
-        for (int mt = 0; mt < kMT; ++mt) {
-          pa[mt][0] = pack_f16x2(s[mt][2 * ks][0], s[mt][2 * ks][1]);
-          pa[mt][1] = pack_f16x2(s[mt][2 * ks][2], s[mt][2 * ks][3]);
-          pa[mt][2] = pack_f16x2(s[mt][2 * ks + 1][0], s[mt][2 * ks + 1][1]);
-          pa[mt][3] = pack_f16x2(s[mt][2 * ks + 1][2], s[mt][2 * ks + 1][3]);
-        }
-        // Keys behind the sequence hold anything, NaN too: their bytes count as zero.
-        const int rk = 16 * ks + 2 * t;  // this lane's keys: rk, rk + 1, rk + 8, rk + 9
-        const bool z0 = key + rk >= it.s.len, z1 = key + rk + 1 >= it.s.len;
-        const bool z2 = key + rk + 8 >= it.s.len, z3 = key + rk + 9 >= it.s.len;
-        uint32_t nans = 0;  // NaN codes of a tile that some rows see only in part
+      for (int mk = 0; mk < 2; ++mk) {
+        if (!((named >> mk) & 1u)) continue;
+        const int rk = 16 * mk + 2 * t;  // this lane's keys: rk, rk + 1, rk + 8, rk + 9
+        uint32_t nans = 0;               // NaN codes of a tile that some rows see only in part
 #pragma unroll
         for (int dg = 0; dg < kD / 32; ++dg) {
           uint32_t w[4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int row = rk + (q & 1) + (q >> 1) * 8;
-            if constexpr (C::kBoxD == 128) {
-              const int half = dg >> 2, chunk = (dg & 3) * 2 + (g >> 2);
-              w[q] = lds32(vt + half * (kTile * 128) + row * 128 + ((chunk ^ (row & 7)) << 4) + (g & 3) * 4);
-            } else {
-              const int chunk = dg * 2 + (g >> 2);
-              w[q] = lds32(vt + row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4) + (g & 3) * 4);
-            }
-          }
-          if (!whole) {
-            w[0] = z0 ? 0u : w[0];
-            w[1] = z1 ? 0u : w[1];
-            w[2] = z2 ? 0u : w[2];
-            w[3] = z3 ? 0u : w[3];
+          for (int q = 0; q < 4; ++q)
+            w[q] = lds32(vt + (v_at[q & 1] ^ ((dg & 3) << 5)) + (dg >> 2) * (kTile * 128) +
+                         (16 * mk + 8 * (q >> 1)) * C::kBoxD);
+          if constexpr (!kWhole) {
+            // Keys behind the sequence hold anything, NaN too: their bytes count as zero.
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
+              if (key + rk + (q & 1) + (q >> 1) * 8 >= it.s.len) w[q] = 0u;
               const uint32_t bad = nan_bytes(w[q]);
               nans |= bad;
               w[q] &= ~((bad >> 7) * 255u);
             }
           }
           // Pairs of keys per head dim: {k0 d0, k1 d0, k0 d1, k1 d1}, {.. d2, .. d3} and the same of k2, k3.
-          const uint32_t lo01 = __byte_perm(w[0], w[1], 0x5140), lo23 = __byte_perm(w[0], w[1], 0x7362);
-          const uint32_t hi01 = __byte_perm(w[2], w[3], 0x5140), hi23 = __byte_perm(w[2], w[3], 0x7362);
-          uint32_t b0[4], b1[4];
-          widen4(lo01, b0[0], b0[1]);
-          widen4(lo23, b0[2], b0[3]);
-          widen4(hi01, b1[0], b1[1]);
-          widen4(hi23, b1[2], b1[3]);
+          uint32_t va[4], vb[4];
+          widen4(__byte_perm(w[0], w[1], 0x5140), va[0], va[1]);
+          widen4(__byte_perm(w[2], w[3], 0x5140), va[2], va[3]);
+          widen4(__byte_perm(w[0], w[1], 0x7362), vb[0], vb[1]);
+          widen4(__byte_perm(w[2], w[3], 0x7362), vb[2], vb[3]);
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-#pragma unroll
-            for (int mt = 0; mt < kMT; ++mt) mma_f16(o[mt][dg * 4 + q], pa[mt], b0[q], b1[q]);
+          for (int n = 0; n < kNT; ++n) {
+            mma_f16(o[2 * dg][n], va, pb[mk][n][0], pb[mk][n][1]);
+            mma_f16(o[2 * dg + 1][n], vb, pb[mk][n][0], pb[mk][n][1]);
+          }
         }
         // A NaN times a masked probability's zero would reach rows that do not see its token, so such
         // codes went in as zeros; the rows that see them get their NaN here.
-        if (__any_sync(0xffffffffu, nans != 0)) {
+        if (!kWhole && __any_sync(0xffffffffu, nans != 0)) {
           for (int kk = 0; kk < 16; ++kk) {
-            const int row = 16 * ks + kk;
+            const int row = 16 * mk + kk;
             if (key + row >= it.s.len) break;
 #pragma unroll
             for (int dg = 0; dg < kD / 32; ++dg) {
-              uint2 w;  // head dims 32 dg + 8 t ..
-              if constexpr (C::kBoxD == 128) {
-                const int half = dg >> 2, chunk = (dg & 3) * 2 + (t >> 1);
-                w = *reinterpret_cast<const uint2*>(vt + half * (kTile * 128) + row * 128 + ((chunk ^ (row & 7)) << 4) +
-                                                    (t & 1) * 8);
-              } else {
-                const int chunk = dg * 2 + (t >> 1);
-                w = *reinterpret_cast<const uint2*>(vt + row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4) + (t & 1) * 8);
-              }
-              const uint32_t n0 = nan_bytes(w.x), n1 = nan_bytes(w.y);
+              const uint32_t bad = nan_bytes(v_word(row, dg));
 #pragma unroll
-              for (int mt = 0; mt < kMT; ++mt)
+              for (int n = 0; n < kNT; ++n)
 #pragma unroll
-                for (int i2 = 0; i2 < 2; ++i2)
+                for (int e = 0; e < 2; ++e)
 #pragma unroll
-                  for (int q = 0; q < 4; ++q) {
-                    const bool seen = key + row < lim[mt][i2];
-                    if (seen && ((n0 >> (8 * q + 7)) & 1u)) o[mt][dg * 4 + q][2 * i2] = __uint_as_float(0x7FC00000u);
-                    if (seen && ((n1 >> (8 * q + 7)) & 1u)) o[mt][dg * 4 + q][2 * i2 + 1] = __uint_as_float(0x7FC00000u);
-                  }
+                  for (int q = 0; q < 4; ++q)
+                    if (key + row < lim[n][e] && ((bad >> (8 * q + 7)) & 1u))
+                      o[2 * dg + (q >> 1)][n][2 * (q & 1) + e] = __uint_as_float(0x7FC00000u);
             }
           }
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[c_slot]);
-      if (++c_slot == kStages) {
-        c_slot = 0;
-        c_phase ^= 1;
-      }
-      if (rw == 0 && i + kStages < my_tiles) ok = issue(i + kStages);
+      release(2 * i + 1);
+    };
+    for (int i = 0; i < my_tiles && ok; ++i) {
+      if (!landed()) break;
+      const float4 h0 = meta[2 * (i % C::kMetas)], h1 = meta[2 * (i % C::kMetas) + 1];
+      const int key = key0 + (i * kKW + kw) * kTile;
+      if (key + kTile <= full_end && __float_as_uint(h0.w) == 3u)
+        tile(std::true_type{}, i, key, h0, h1);
+      else
+        tile(std::false_type{}, i, key, h0, h1);
     }
 
     // ---------------------------------------------------------------- join the key groups
 #pragma unroll
-    for (int mt = 0; mt < kMT; ++mt)
+    for (int n = 0; n < kNT; ++n)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        l[mt][i] += __shfl_xor_sync(0xffffffffu, l[mt][i], 1);
-        l[mt][i] += __shfl_xor_sync(0xffffffffu, l[mt][i], 2);
-        const int r = rw * C::kRowsPerWarp + mt * 16 + g + 8 * i;
-        if (t == 0) {
-          s_m[kw * kRows + r] = m[mt][i];
-          s_l[kw * kRows + r] = l[mt][i];
+      for (int e = 0; e < 2; ++e) {
+        l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 4);
+        l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 8);
+        l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 16);
+        const int r = rw * C::kRowsPerWarp + n * 8 + 2 * t + e;
+        if (g == 0) {
+          s_m[kw * kRows + r] = m[n][e];
+          s_l[kw * kRows + r] = l[n][e];
         }
       }
     __syncthreads();  // every tile has been read: the ring's memory is free
     float* merge = reinterpret_cast<float*>(smem);
 #pragma unroll
-    for (int mt = 0; mt < kMT; ++mt)
+    for (int n = 0; n < kNT; ++n)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = rw * C::kRowsPerWarp + mt * 16 + g + 8 * i;
+      for (int e = 0; e < 2; ++e) {
+        const int r = rw * C::kRowsPerWarp + n * 8 + 2 * t + e;
         float mx = s_m[r];
 #pragma unroll
         for (int k = 1; k < kKW; ++k) mx = fmaxf(mx, s_m[k * kRows + r]);
-        const float w = mx == -INFINITY ? 1.0f : exp2f(m[mt][i] - mx);
-        float* dst = merge + (size_t)(kw * kRows + r) * C::kPitch + 8 * t;
+        const float w = mx == -INFINITY ? 1.0f : exp2f(m[n][e] - mx);
+        float* dst = merge + (size_t)(kw * kRows + r) * C::kPitch + 4 * g;
 #pragma unroll
-        for (int dg = 0; dg < kD / 32; ++dg) {
-          // columns 2 t and 2 t + 1 of the four products: head dims 32 dg + 8 t + {0 .. 3}, {4 .. 7}
-          float4 lo, hi;
-          lo.x = o[mt][dg * 4 + 0][2 * i] * w;
-          lo.y = o[mt][dg * 4 + 1][2 * i] * w;
-          lo.z = o[mt][dg * 4 + 2][2 * i] * w;
-          lo.w = o[mt][dg * 4 + 3][2 * i] * w;
-          hi.x = o[mt][dg * 4 + 0][2 * i + 1] * w;
-          hi.y = o[mt][dg * 4 + 1][2 * i + 1] * w;
-          hi.z = o[mt][dg * 4 + 2][2 * i + 1] * w;
-          hi.w = o[mt][dg * 4 + 3][2 * i + 1] * w;
-          *reinterpret_cast<float4*>(dst + dg * 32) = lo;
-          *reinterpret_cast<float4*>(dst + dg * 32 + 4) = hi;
-        }
+        for (int dg = 0; dg < kD / 32; ++dg)
+          *reinterpret_cast<float4*>(dst + dg * 32) = make_float4(o[2 * dg][n][e] * w, o[2 * dg][n][2 + e] * w,
+                                                                  o[2 * dg + 1][n][e] * w, o[2 * dg + 1][n][2 + e] * w);
       }
     __syncthreads();
     const bool complete = kb0 == 0 && kb1 == it.key_blocks;
@@ -717,97 +727,111 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
   }
 }
 
-// Joins the partials of the items cut by run borders, in key order.  One warp per row: a lane weighs
-// every 32nd partial, then the lanes take the head dims and add all partials in order.
-// blockIdx.x: kv head and group of kJoinRows rows of the item list; y: sequence.
-constexpr int kJoinRows = 4;
-template <class C>
-__global__ void __launch_bounds__(32 * kJoinRows) k_attn_kv8_join(const AttnArgs a, const int groups) {
-  constexpr int kD = C::kD, kRows = C::kRows, kPer = kD / 32;
-  __shared__ float s_w[kJoinRows][64];
+// Joins the partials of the items cut by run borders.  kJW warps per row take its partials in turn
+// (warp w every kJW-th, in key order), then their sums are added in order.
+constexpr int kJoinWarps = 8;
+template <class C, int kJW>
+__global__ void __launch_bounds__(32 * kJoinWarps) k_attn_kv8_join(const AttnArgs a, const int most_rows) {
+  constexpr int kD = C::kD, kRows = C::kRows, kPer = kD / 32, kRowsPerCta = kJoinWarps / kJW;
+  __shared__ float s_acc[kJoinWarps][kD];
+  __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
   griddep_wait();
   griddep_launch_dependents();
-  const int b = blockIdx.y, h = blockIdx.x / groups, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rr = (blockIdx.x % groups) * kJoinRows + warp;  // row of the (sequence, kv head)
+  const int lane = threadIdx.x & 31, slot = threadIdx.x >> 5, warp = slot % kJW, first = slot - warp;
+  const int b = blockIdx.y, x = blockIdx.x * kRowsPerCta + slot / kJW;
+  const int h = x / most_rows, rr = x - h * most_rows;  // kv head, row of the (sequence, kv head)
   const Items it = items_of<C>(a, b);
-  const int rt = rr / kRows, r = rr % kRows;
-  if (rr >= it.s.count * a.group) return;
-  long long W = 0, base = 0;
-  for (int q = lane; q < a.batch; q += 32) {
-    const long long n = items_of<C>(a, q).units(a.kv_heads);
-    W += n;
-    base += q < b ? n : 0;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    W += __shfl_xor_sync(0xffffffffu, W, o);
-    base += __shfl_xor_sync(0xffffffffu, base, o);
-  }
-  const int runs = runs_used(W, a.runs, a.min_units);
-  const long long u0 = base + (long long)(h * it.row_tiles + rt) * it.key_blocks, u1 = u0 + it.key_blocks;
-  // Run of unit u: the last r with W r / runs <= u.
-  auto run_of = [&](long long u) {
-    int q = (int)((u * runs) / W);
-    while (W * (q + 1) / runs <= u) ++q;
-    while (W * q / runs > u) --q;
-    return q;
-  };
-  const int r0 = run_of(u0), r1 = run_of(u1 - 1);
+  if (h >= a.kv_heads || rr >= it.s.count * a.group) return;  // (all warps of a row together)
+  const int rt = rr / kRows, r = rr - rt * kRows;
+  const int2 W = count_units<C>(a, b, lane);
+  const Runs runs = runs_of(W.x, a.runs);
+  const int u0 = W.y + (h * it.row_tiles + rt) * it.key_blocks;
+  const int r0 = runs.of(u0), r1 = runs.of(u0 + it.key_blocks - 1);
   if (r0 == r1) return;  // written by its CTA
-  const int slot0 = 2 * r0 + (W * r0 / runs == u0 ? 0 : 1);
+  const int slot0 = 2 * r0 + (runs.begin(r0) == u0 ? 0 : 1);
   const float* ml = a.partial + (size_t)2 * a.runs * kRows * kD;
   const float* ll = ml + (size_t)2 * a.runs * kRows;
-  auto at = [&](int c) { return (size_t)(c == r0 ? slot0 : 2 * c) * kRows + r; };
-  float mx = -INFINITY;
-  for (int c = r0 + lane; c <= r1; c += 32) mx = fmaxf(mx, ml[at(c)]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  float sum = 0.0f, acc[kPer];
+  float mx = -INFINITY, sum = 0.0f, acc[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) acc[i] = 0.0f;
-  for (int c0 = r0; c0 <= r1; c0 += 64) {
-    __syncwarp();
+  constexpr int kFlight = kJW == 1 ? 4 : 8;  // partials in flight per warp
+  for (int c0 = r0 + warp; c0 <= r1; c0 += kFlight * kJW) {
+    float pm[kFlight], pl[kFlight], v[kFlight][kPer];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int c = c0 + 32 * j + lane;
-      float w = 0.0f;
+    for (int k = 0; k < kFlight; ++k) {
+      const int c = c0 + k * kJW;
+      pm[k] = -INFINITY;
+      pl[k] = 0.0f;
       if (c <= r1) {
-        w = mx == -INFINITY ? 1.0f : exp2f(ml[at(c)] - mx);
-        sum += w * ll[at(c)];
-      }
-      s_w[warp][32 * j + lane] = w;
-    }
-    __syncwarp();
-    const int n = min(64, r1 - c0 + 1);
-#pragma unroll 8
-    for (int c = 0; c < n; ++c) {
-      const float w = s_w[warp][c];
-      const float* src = a.partial + at(c0 + c) * kD + lane * kPer;
+        const size_t at = (size_t)(c == r0 ? slot0 : 2 * c) * kRows + r;
+        pm[k] = ml[at];
+        pl[k] = ll[at];
 #pragma unroll
-      for (int i = 0; i < kPer; i += 2) {
-        const float2 v = *reinterpret_cast<const float2*>(src + i);
-        acc[i] = fmaf(w, v.x, acc[i]);
-        acc[i + 1] = fmaf(w, v.y, acc[i + 1]);
+        for (int i = 0; i < kPer; i += 2) {
+          const float2 x = *reinterpret_cast<const float2*>(a.partial + at * kD + lane * kPer + i);
+          v[k][i] = x.x;
+          v[k][i + 1] = x.y;
+        }
       }
     }
+    float m_new = mx;
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k) m_new = fmaxf(m_new, pm[k]);
+    // Without any maximum there is nothing to weigh (sums of zero, or of NaN).
+    const float alpha = m_new == -INFINITY ? 1.0f : exp2f(mx - m_new);
+    sum *= alpha;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) acc[i] *= alpha;
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k) {
+      if (c0 + k * kJW > r1) break;
+      const float w = m_new == -INFINITY ? 1.0f : exp2f(pm[k] - m_new);
+      sum = fmaf(w, pl[k], sum);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) acc[i] = fmaf(w, v[k][i], acc[i]);
+    }
+    mx = m_new;
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  const float inv = sum == 0.0f ? 0.0f : kUnbias / sum;  // a row that sees nothing: zeros
   const size_t row = (size_t)(it.s.begin + rr / a.group);
   const int head = h * a.group + rr % a.group;
-  const size_t o = row * (size_t)a.ldo + (size_t)head * kD + lane * kPer;
+  const size_t o = row * (size_t)a.ldo + (size_t)head * kD;
+  if constexpr (kJW > 1) {
+    if (lane == 0) {
+      s_m[slot] = mx;
+      s_l[slot] = sum;
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) s_acc[slot][lane * kPer + i] = acc[i];
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + first / kJW), "n"(32 * kJW) : "memory");
+    if (warp != 0) return;
+    mx = s_m[first];
+#pragma unroll
+    for (int w = 1; w < kJW; ++w) mx = fmaxf(mx, s_m[first + w]);
+    sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) acc[i] = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kJW; ++w) {
+      const float weight = mx == -INFINITY ? 1.0f : exp2f(s_m[first + w] - mx);
+      sum = fmaf(weight, s_l[first + w], sum);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) acc[i] = fmaf(weight, s_acc[first + w][lane * kPer + i], acc[i]);
+    }
+  }
+  const float inv = sum == 0.0f ? 0.0f : kUnbias / sum;  // a row that sees nothing: zeros
 #pragma unroll
   for (int i = 0; i < kPer; i += 2) {
     if (a.out_bf16)
-      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + o + i) = pack_bf16x2(acc[i] * inv, acc[i + 1] * inv);
+      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + o + lane * kPer + i) =
+          pack_bf16x2(acc[i] * inv, acc[i + 1] * inv);
     else
-      *reinterpret_cast<float2*>(static_cast<float*>(a.out) + o + i) = make_float2(acc[i] * inv, acc[i + 1] * inv);
+      *reinterpret_cast<float2*>(static_cast<float*>(a.out) + o + lane * kPer + i) =
+          make_float2(acc[i] * inv, acc[i + 1] * inv);
   }
   if (a.lse && lane == 0) a.lse[row * a.q_heads + head] = sum == 0.0f ? -INFINITY : kLn2 * (mx + log2f(sum));
 }
 
-constexpr int kMaxRuns = 444;  // 148 SMs x 3 CTAs
+constexpr int kMaxRuns = 592;  // 148 SMs x 4 CTAs
 
 template <class C>
 cudaError_t launch_cfg(const AttnKv8Launch& L, cudaStream_t stream) {
@@ -851,7 +875,6 @@ cudaError_t launch_cfg(const AttnKv8Launch& L, cudaStream_t stream) {
   }
   const int slots = sm_count() * occ[dev];
   a.runs = slots < kMaxRuns ? slots : kMaxRuns;
-  a.min_units = 1;
 
   CUtensorMap tm_k, tm_v;
   const uint64_t rows = (uint64_t)L.num_pages * L.kv_heads * L.page_size;
@@ -875,25 +898,31 @@ cudaError_t launch_cfg(const AttnKv8Launch& L, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   // No sequence can be longer than its page table: when that is one unit, no item is ever cut.
   if ((long long)L.max_pages * L.page_size <= C::kUnit) return cudaSuccess;
-  const long long groups = ((long long)L.max_q_len * a.group + kJoinRows - 1) / kJoinRows;
-  if (groups * L.kv_heads >= (1LL << 31)) return cudaErrorInvalidConfiguration;
-  cfg.gridDim = dim3((unsigned)(groups * L.kv_heads), (unsigned)L.batch);
-  cfg.blockDim = dim3(32 * kJoinRows);
+  const long long rows_most = (long long)L.max_q_len * a.group, rows_all = rows_most * L.kv_heads;
+  if (rows_all >= (1LL << 31) - 8) return cudaErrorInvalidConfiguration;
+  // With at least a quarter as many items as runs an item has about four partials at most: a warp per row.
+  const bool few = (long long)L.batch * L.kv_heads * 4 >= a.runs;
+  cfg.gridDim = dim3((unsigned)(few ? (rows_all + kJoinWarps - 1) / kJoinWarps : rows_all), (unsigned)L.batch);
+  cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, k_attn_kv8_join<C>, a, (int)groups);
+  return few ? cudaLaunchKernelEx(&cfg, k_attn_kv8_join<C, 1>, a, (int)rows_most)
+             : cudaLaunchKernelEx(&cfg, k_attn_kv8_join<C, kJoinWarps>, a, (int)rows_most);
 }
 
 // Rows of an item by the most rows a sequence can have (queries times heads per kv head).
 template <int kD>
 cudaError_t launch_rows(const AttnKv8Launch& L, cudaStream_t stream) {
   const long long rows = (long long)L.max_q_len * (L.q_heads / L.kv_heads);
-  constexpr bool kWide = kD == 256;  // two 16-row tiles per warp would not fit its registers
-  if (rows <= 16) return launch_cfg<AttnCfg<kD, 1, 1, 4, kD == 64 ? 4 : 2, kWide ? 1 : 3>>(L, stream);
-  if (rows <= 32) return launch_cfg<AttnCfg<kD, kWide ? 1 : 2, kWide ? 2 : 1, 4, kD == 64 ? 4 : 2, kWide ? 1 : 2>>(L, stream);
-  return launch_cfg<AttnCfg<kD, kWide ? 1 : 2, kWide ? 4 : 2, 2, kD == 64 ? 4 : 3, kWide ? 1 : 2>>(L, stream);
+  // Up to two 8-row tiles per warp (three in the widest form) keep the accumulators, kD / 4 registers
+  // each, beside 12 warps per SM; further rows take further warps that read the same tiles.
+  constexpr int kSlots = kD == 64 ? 4 : 3;
+  if (rows <= 8) return launch_cfg<AttnCfg<kD, 1, 1, 4, kSlots, kD == 256 ? 2 : 4>>(L, stream);
+  if (rows <= 16) return launch_cfg<AttnCfg<kD, 2, 1, 4, kSlots, kD == 256 ? 1 : 3>>(L, stream);
+  if (rows <= 32 || kD == 256) return launch_cfg<AttnCfg<kD, 2, 2, 2, 4, kD == 256 ? 1 : 3>>(L, stream);
+  return launch_cfg<AttnCfg<kD == 256 ? 128 : kD, 3, 2, 2, 4, 3>>(L, stream);
 }
 
-int rows_per_item(long long rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+int rows_per_item(long long rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 48; }
 
 }  // namespace
 
