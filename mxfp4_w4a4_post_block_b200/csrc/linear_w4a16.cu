@@ -7,25 +7,27 @@
 // result: NVFP4).  With so few tokens the weights' bytes are the work, so nothing is done to them:
 // they go from memory by TMA straight into block-scaled 4-bit matrix instructions (kind::mxf4,
 // kind::mxf4nvf4), 128 weight rows on the M side.  The tokens' precision comes from several columns
-// instead of wider elements: y / scale is written as a sum of E2M1 digits,
-//   r_0 = y / 2^e,  q_p = E2M1(r_p),  r_{p+1} = f_p (r_p - q_p),  f_0 = 4, f_p = 8,
+// instead of wider elements: y / 2^e, 2^e the scale of y's block, is rounded to a fixed-point number
+// and written in radix 8 with the digits -4 .. 3, which are E2M1 values,
+//   y = 2^e (d_0 + d_1 / 8 + d_2 / 64 + ..),   |y| < 2 * 2^e,
 // one column of the N side per token and digit, all digits of a block under the block's scale, and
-// the digits' accumulators are added with the weights 1, 1/4, 1/32, .. in the epilogue.  |r_0| <= 6
-// leaves a remainder of at most 1, so |r_1| <= 4, remainder at most 1/2, |r_2| <= 4 and so on: three
-// bits a digit, exact arithmetic throughout.  Five digits (2^-13 of the block's largest value) serve a
-// bf16 output, eight (2^-22) an fp32 one; sixteen tokens then are 80 or 128 of the 256 columns an
-// instruction can have, and the tensor pipe still waits for memory.  (With the weights widened to f16 in
-// registers for m16n8k16 instructions, the same products were bound by the conversions: 4 tokens x
-// 4096 x 24576 took 30 us, 16 tokens 113 us.)
+// the digits' accumulators are added with the weights 1, 1/8, 1/64, .. in the epilogue.  Five digits
+// (2^-13 of the block's largest value) serve a bf16 output, eight (2^-22) an fp32 one; sixteen tokens
+// then are 80 or 128 of the 256 columns an instruction can have, and the tensor pipe still waits for
+// memory.  (With the weights widened to f16 in registers for m16n8k16 instructions, the same products
+// were bound by the conversions: 4 tokens x 4096 x 24576 took 30 us, 16 tokens 113 us.)
 //
 // A CTA makes its tokens' digits once, keeps them and their scales (shared memory, TMEM), and walks
-// 128-row tiles of the weights: warp 0 loads stages of K = 256 (16 KB of codes by TMA with the
-// 128-byte swizzle, 512-byte scale tiles) into a ring, warp 1 copies their scales into TMEM and issues
-// four MMAs per stage into one of two accumulators, warps 2-5 drain the other.  When the digits do not
-// fit, or when there are fewer tiles than SMs, the CTAs of a cluster split K; their sums meet in
-// distributed shared memory, rank after rank.
+// 128-row tiles of the weights.  One warp loads stages of K = 256 (16 KB of codes by TMA with the
+// 128-byte swizzle, 512-byte scale tiles) into a ring, one copies their scales into TMEM and issues four
+// MMAs per stage into one of two accumulators, four drain the other.  Sixteen warps make the digits,
+// stage after stage, so the first tile's products begin with the first stage's.  The CTAs of a cluster
+// split K where the digits would not fit otherwise or where it balances the tiles over the SMs
+// (launch_cfg); their sums meet in distributed shared memory, rank after rank.
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
+#include <utility>
 
 #include "host_util.h"
 #include "kernels.h"
@@ -35,15 +37,17 @@
 namespace batq {
 namespace {
 
-constexpr int kWarps = 10;                       // loads, MMA, 8 that make the digits (4 of them drain)
-constexpr int kThreads = 32 * kWarps;
-constexpr int kMakers = 32 * (kWarps - 1);       // all but the load warp make digits
+constexpr int kMakerWarps = 16;                  // make the digits; then the first four drain the accumulators
+constexpr int kMakers = 32 * kMakerWarps;
+constexpr int kLoadWarp = kMakerWarps, kMmaWarp = kMakerWarps + 1;
+constexpr int kThreads = 32 * (kMakerWarps + 2);
 constexpr int kRows = 128;                       // weight rows per tile
 constexpr int kStageK = 256;                     // K elements per stage
 constexpr int kStageBytes = kRows * kStageK / 2;
 constexpr int kSfAtom = 512;
 constexpr int kMaxRing = 10;
-constexpr int kMaxParts = 8;
+constexpr int kMaxPasses = 32;                   // of the makers over their items (the digits' space allows 14)
+constexpr int kPartsBf16 = 5, kPartsF32 = 8;     // digits by output type
 
 struct W4Args {
   const void* X;
@@ -82,25 +86,22 @@ __device__ __forceinline__ void load_x8(const W4Args& a, int s, int k, float (&v
   }
 }
 
-// Values of eight packed E2M1 codes.  (Each byte is shifted down first: taken out of one 32-bit move
-// into four 8-bit registers, the upper two came back as zeros.)
-__device__ __forceinline__ void e2m1x8_values(uint32_t w, float (&v)[8]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    asm("{\n\t.reg .b8 c;\n\t.reg .b32 hh;\n\t.reg .b16 l, h;\n\t"
-        "cvt.u8.u32 c, %2;\n\t"
-        "cvt.rn.f16x2.e2m1x2 hh, c;\n\t"
-        "mov.b32 {l, h}, hh;\n\t"
-        "cvt.f32.f16 %0, l;\n\t"
-        "cvt.f32.f16 %1, h;\n\t}"
-        : "=f"(v[2 * i]), "=f"(v[2 * i + 1])
-        : "r"(w >> (8 * i)));
-}
+// Smallest e >= -126 with a < 2 * 2^e, a finite and >= 0.
+__device__ __forceinline__ int digit_exponent(float a) { return max((int)(__float_as_uint(a) >> 23) - 127, -126); }
 
-// Smallest e >= -126 with a <= 6 * 2^e (6 = 1.5 * 2^2), a finite and >= 0.
-__device__ __forceinline__ int digit_exponent(float a) {
-  const uint32_t u = __float_as_uint(a);
-  return max((int)(u >> 23) - 127 - 2 + ((u & 0x7FFFFFu) > 0x400000u ? 1 : 0), -126);
+// E2M1 codes of the digit whose three bits (the digit plus four) stand at bit kAt of eight fixed-point
+// numbers, v[j] holding number 2 j in its low half and 2 j + 1 in its high half.  The bits select the
+// code by byte permutes: even numbers' codes from one table, odd numbers' from the same in the high nibble.
+template <int kAt>
+__device__ __forceinline__ uint32_t digit_codes(const uint32_t (&v)[4]) {
+  uint32_t sel = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t t = kAt >= 4 * j ? v[j] >> (kAt >= 4 * j ? kAt - 4 * j : 0) : v[j] << (kAt < 4 * j ? 4 * j - kAt : 0);
+    sel |= t & (0x00070007u << (4 * j));
+  }
+  constexpr uint32_t kNeg = 0x0A0C0D0Eu, kPos = 0x05040200u;  // codes of -4 .. -1 and of 0 .. 3
+  return __byte_perm(kNeg, kPos, sel) | __byte_perm(kNeg << 4, kPos << 4, sel >> 16);
 }
 
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
@@ -129,10 +130,20 @@ __device__ __forceinline__ bool mbar_wait_warp_cluster(uint64_t* bar, uint32_t p
   return __all_sync(0xffffffffu, done != 0) != 0;
 }
 
+// f(0), f(1), .. as compile-time numbers.
+template <int kCount, class F, int... kI>
+__device__ __forceinline__ void for_digits_impl(F&& f, std::integer_sequence<int, kI...>) {
+  (f(std::integral_constant<int, kI>{}), ...);
+}
+template <int kCount, class F>
+__device__ __forceinline__ void for_digits(F&& f) {
+  for_digits_impl<kCount>(f, std::make_integer_sequence<int, kCount>{});
+}
+
 // kN consecutive fp32 columns of this thread's TMEM lane.
 template <int kN>
 __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[kN]) {
-  static_assert(kN == 1 || kN == 2 || kN == 4 || kN == 8 || kN == 16, "columns");
+  static_assert(kN == 1 || kN == 2 || kN == 4 || kN == 8, "columns");
   if constexpr (kN == 1)
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r[0]) : "r"(taddr));
   else if constexpr (kN == 2)
@@ -141,16 +152,14 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[kN]) 
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(taddr));
-  else if constexpr (kN == 8)
+  else
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                  : "r"(taddr));
-  else
-    tmem_ld_16cols(taddr, r);
 }
 
-// kSp: tokens padded to a power of two (columns of a digit).
-template <int kSp, bool kNv>
+// kSp: tokens padded to a power of two (columns of a digit); kParts: digits.
+template <int kSp, bool kNv, int kParts>
 __global__ void __launch_bounds__(kThreads, 1)
     k_linear_w4a16(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ W4Args a) {
   constexpr int kAtoms = kNv ? 4 : 2;             // scale tiles (four scale columns) of a stage
@@ -170,7 +179,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* acc_full = empty + kMaxRing;
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* sums_ready = acc_empty + 2;
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sums_ready + 2);
+  uint64_t* made = sums_ready + 2;                                         // [kMaxPasses] digits of a pass
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(made + kMaxPasses);
 
   uint32_t csize, crank;
   asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(csize));
@@ -186,6 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
+    for (int i = 0; i < kMaxPasses; ++i) mbar_init(&made[i], kMakerWarps);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
       mbar_init(&acc_empty[i], 4);
@@ -194,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_barrier_init();
   }
   if (tid < 16) s_amax[tid] = 0u;
-  if (warp == 1) {
+  if (warp == kMmaWarp) {
     tmem_alloc(tmem_holder, 512);
     tmem_relinquish();
   }
@@ -206,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_holder;
 
-  if (warp == 0) {
+  if (warp == kLoadWarp) {
     // ------------------------------ loads ------------------------------
     if (lane == 0) {
       int s = 0;
@@ -230,181 +241,216 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
     }
+  } else if (warp == kMmaWarp) {
+    // ------------------------------ scale copies and MMAs ------------------------------
+    // One thread's copies and MMAs run in order.  (Another warp issuing the copies a stage ahead, as in
+    // the GEMMs with wide tiles, costs a commit and a barrier per stage: 9.8 instead of 8.4 us for one
+    // tile of K = 4096.)  The loop runs warp-wide (warp-uniform state) with one elected lane issuing.
+    const bool issuer = elect_one();
+    const int per_stage = 32 * a.S;  // items of a stage
+    int s = 0, it = 0, passes = 0;   // passes: digits known to be made
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int tile = cluster; tile < a.tiles && ok; tile += clusters, ++it) {
+      const int buf = it & 1;
+      if (!mbar_wait_warp(&acc_empty[buf], ((it >> 1) & 1) ^ 1)) {
+        if (issuer) set_error(a.err, kErrDrainTimeout);
+        break;
+      }
+      tc_fence_after_sync();
+      const uint32_t t_acc = tmem + buf * a.acc_stride;
+      for (int st = st0; st < st1; ++st) {
+        if (it == 0) {  // the stage's digits and their scales
+          const int need = (min((st - st0 + 1) * per_stage, a.S * ((k1 - k0) >> 3)) + kMakers - 1) / kMakers;
+          for (; passes < need && ok; ++passes) ok = mbar_wait_warp(&made[passes], 0);
+        }
+        if (!ok || !mbar_wait_warp(&full[s], ph)) {
+          if (issuer) set_error(a.err, kErrDataTimeout);
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        if (issuer) {
+          const int nmma = min(4, (a.N - st * kStageK) >> 6);
+          const int atoms = kNv ? nmma : (nmma + 1) >> 1;
+          const uint32_t tsw = tmem + a.t_sw + s * (4 * kAtoms);
+          const uint32_t tsx = tmem + a.t_sx + (st - st0) * (4 * kAtoms);
+          const uint64_t dsw = sdesc_sf_atom(smem_u32(s_sw + s * kSfBytes));
+          const uint64_t dsx = sdesc_sf_atom(smem_u32(s_sx + (st - st0) * kSfBytes));
+          for (int i = 0; i < atoms; ++i) {
+            tc_cp_32x128b_warpx4(tsw + 4 * i, dsw + (uint64_t)(i * (kSfAtom >> 4)));
+            if (it == 0) tc_cp_32x128b_warpx4(tsx + 4 * i, dsx + (uint64_t)(i * (kSfAtom >> 4)));
+          }
+          const uint64_t dw = sdesc_kmajor_sw128(smem_u32(s_w + s * kStageBytes));
+          const uint64_t dx = sdesc_kmajor_sw128(smem_u32(s_x + (size_t)(st - st0) * (a.n * 128)));
+          for (int j = 0; j < nmma; ++j) {
+            const uint32_t acc = (st > st0 || j > 0) ? 1u : 0u;
+            if constexpr (kNv)
+              tc_mma_nvf4(t_acc, dw + (uint64_t)(j * 2), dx + (uint64_t)(j * 2), idesc_nvf4(kRows, a.n), tsw + 4 * j,
+                          tsx + 4 * j, acc);
+            else
+              tc_mma_mxf4(t_acc, dw + (uint64_t)(j * 2), dx + (uint64_t)(j * 2),
+                          idesc_mxf4(a.n, (2 * j) & 3, (2 * j) & 3), tsw + 4 * (j >> 1), tsx + 4 * (j >> 1), acc);
+          }
+          tc_commit(&empty[s]);
+          if (st == st1 - 1) tc_commit(&acc_full[buf]);
+        }
+        __syncwarp();
+        if (++s == a.ring) {
+          s = 0;
+          ph ^= 1;
+        }
+      }
+    }
   } else {
     // ------------------------------ digits ------------------------------
     // A thread makes row b (eight values) of one 4 x 8 block of one token: u = column b of B^T against
     // the block's four rows, y = u A (A from the parameter bank).
-    const int id = tid - 32;
+    const int id = tid;
     const int rows = ((k1 - k0) >> 5) * 4;  // of each token
     if constexpr (kNv) {
       // E4M3 scales span 17 powers of two, so a token's blocks are scaled relative to a bound of its
       // largest magnitude: |y| <= max |x| |B|_1 |A|_1 over its blocks.
-      for (int s = 0; s < a.S; ++s) {
-        float m = 0.0f;
-        for (int x0 = id; x0 < rows; x0 += 4 * kMakers) {
-          float v[4][8];
-          float4 br[4];
+      // A warp takes 32 rows of one token at a time, four such pieces in flight.
+      const int pieces = (rows + 31) >> 5;
+      for (int p0 = warp; p0 < a.S * pieces; p0 += 4 * kMakerWarps) {
+        float v[4][8];
+        float4 br[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {  // four rows in flight
-            const int x = x0 + j * kMakers;
-            if (x < rows) {
-              load_x8(a, s, k0 + x * 8, v[j]);
-              if (a.transform) br[j] = __ldg(reinterpret_cast<const float4*>(a.B + (size_t)(k0 >> 3) * 4 + x * 4));
-            }
+        for (int j = 0; j < 4; ++j) {
+          const int p = p0 + j * kMakerWarps, s = p / pieces, x = (p - s * pieces) * 32 + lane;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[j][i] = 0.0f;
+          br[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (s < a.S && x < rows) {
+            load_x8(a, s, k0 + x * 8, v[j]);
+            if (a.transform) br[j] = __ldg(reinterpret_cast<const float4*>(a.B + (size_t)(k0 >> 3) * 4 + x * 4));
           }
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (x0 + j * kMakers < rows) {
-              float mj = 0.0f;
-#pragma unroll
-              for (int i = 0; i < 8; ++i) mj = fabsf(v[j][i]) <= 3.402823466e38f ? fmaxf(mj, fabsf(v[j][i])) : mj;
-              if (a.transform)
-                mj *= 4.0f * a.a_norm *
-                      fmaxf(fmaxf(fabsf(br[j].x), fabsf(br[j].y)), fmaxf(fabsf(br[j].z), fabsf(br[j].w)));
-              m = fmaxf(m, fminf(mj, 3.402823466e38f));
-            }
         }
-        const unsigned bits = __reduce_max_sync(0xffffffffu, __float_as_uint(m));  // not negative: ordered as bits
-        if (lane == 0) atomicMax(&s_amax[s], bits);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int s = (p0 + j * kMakerWarps) / pieces;
+          float m = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) m = fabsf(v[j][i]) <= 3.402823466e38f ? fmaxf(m, fabsf(v[j][i])) : m;
+          if (a.transform)
+            m *= 4.0f * a.a_norm * fmaxf(fmaxf(fabsf(br[j].x), fabsf(br[j].y)), fmaxf(fabsf(br[j].z), fabsf(br[j].w)));
+          // (not negative: ordered as bits)
+          const unsigned bits = __reduce_max_sync(0xffffffffu, __float_as_uint(fminf(m, 3.402823466e38f)));
+          if (lane == 0 && s < a.S) atomicMax(&s_amax[s], bits);
+        }
       }
       asm volatile("bar.sync 1, %0;" ::"n"(kMakers) : "memory");
       if (id < a.S) s_xf[id] = e8m0_value((uint32_t)(127 + digit_exponent(__uint_as_float(s_amax[id])))) * 0.00390625f;
     }
-    for (int s = 0; s < a.S; ++s) {
-      int e_tok = 0;
-      if constexpr (kNv) e_tok = digit_exponent(__uint_as_float(s_amax[s]));
-      for (int x0 = 0; x0 < rows; x0 += kMakers) {  // (whole warps: rows of a block meet in shuffles)
-        const int x = x0 + id;
-        const bool live = x < rows;
-        const int b = x & 3, blk = x >> 2, k = k0 + blk * 32;
-        float y[8];
+    // Items are rows in the order of the stages, within a stage token after token: 32 rows (8 blocks) of
+    // each.  A warp's items are one token's, and the rows of a block meet in its shuffles.
+    const int stage_rows = 32, items = a.S * rows;
+    const int whole = (rows >> 5) * stage_rows * a.S;  // items of whole stages; the last may have fewer rows
+    auto place = [&](int item, int& s, int& x) {      // token and row of an item
+      if (item < whole) {
+        const int st = item / (stage_rows * a.S), r = item - st * (stage_rows * a.S);
+        s = r >> 5;
+        x = st * stage_rows + (r & 31);
+      } else {
+        const int left = rows & 31, r = item - whole;
+        s = r / left;
+        x = (rows & ~31) + r - s * left;
+      }
+    };
+    int pass = 0;
+    for (int i0 = 0; i0 < items; i0 += kMakers, ++pass) {
+      const int item = i0 + id;
+      const bool live = item < items;
+      int s = 0, x = 0;
+      if (live) place(item, s, x);
+      const int b = x & 3, blk = x >> 2, k = k0 + blk * 32;
+      float y[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = 0.0f;
-        if (live) {
-          if (a.transform) {
-            float u[8];
+      for (int i = 0; i < 8; ++i) y[i] = 0.0f;
+      if (live) {
+        if (a.transform) {
+          float u[8];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              float v[8];
-              load_x8(a, s, k + r * 8, v);
-              const float w = __ldg(a.B + (size_t)(k >> 5) * 16 + r * 4 + b);
+          for (int r = 0; r < 4; ++r) {
+            float v[8];
+            load_x8(a, s, k + r * 8, v);
+            const float w = __ldg(a.B + (size_t)(k >> 5) * 16 + r * 4 + b);
 #pragma unroll
-              for (int c = 0; c < 8; ++c) u[c] = r == 0 ? w * v[c] : fmaf(w, v[c], u[c]);
-            }
-#pragma unroll
-            for (int d = 0; d < 8; ++d) {
-              y[d] = u[0] * a.A[d];
-#pragma unroll
-              for (int c = 1; c < 8; ++c) y[d] = fmaf(u[c], a.A[c * 8 + d], y[d]);
-            }
-          } else {
-            load_x8(a, s, k + b * 8, y);
+            for (int c = 0; c < 8; ++c) u[c] = r == 0 ? w * v[c] : fmaf(w, v[c], u[c]);
           }
-        }
-        // The block's (NVFP4: its half's) largest magnitude; NaN and infinities win.
-        unsigned top = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(y[i]) & 0x7FFFFFFFu);
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        if constexpr (!kNv) top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const bool finite = top < 0x7F800000u;
-        int e = digit_exponent(__uint_as_float(finite ? top : 0u));
-        if constexpr (kNv) e = max(e, e_tok - 17);
-        const float inv = e8m0_value((uint32_t)max(127 - e, 0));
-        uint8_t* dst = s_x + (size_t)(blk >> 3) * (a.n * 128) + b * 4;
-        // Scale byte of column r: four scale columns to a tile, row r % 32, then r / 32, then the scale column.
-        const int col = kNv ? blk * 2 + (b >> 1) : blk;
-        uint8_t* sc = s_sx + (col >> 2) * kSfAtom + (col & 3);
-        uint8_t byte;
-        if constexpr (kNv) {
-          const int E = e - e_tok + 8;  // -9 .. 8: the E4M3 power of two
-          byte = (uint8_t)(!finite ? 0x7F : E >= -6 ? (E + 7) << 3 : 1 << (E + 9));
+          for (int d = 0; d < 8; ++d) {
+            y[d] = u[0] * a.A[d];
+#pragma unroll
+            for (int c = 1; c < 8; ++c) y[d] = fmaf(u[c], a.A[c * 8 + d], y[d]);
+          }
         } else {
-          byte = (uint8_t)(finite ? e + 127 : 255);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = finite ? y[i] * inv : 0.0f;
-        if (live) {
-          float f = 4.0f;
-          for (int p = 0; p < a.parts; ++p) {
-            const int r = p * kSp + s;
-            const uint32_t w = e2m1x8(y[0], y[1], y[2], y[3], y[4], y[5], y[6], y[7]);
-            *reinterpret_cast<uint32_t*>(dst + r * 128 + (((blk & 7) ^ (r & 7)) << 4)) = w;
-            if (kNv ? (b & 1) == 0 : b == 0) sc[(r & 31) * 16 + (r >> 5) * 4] = byte;
-            float q[8];
-            e2m1x8_values(w, q);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = (y[i] - q[i]) * f;
-            f = 8.0f;
-          }
+          load_x8(a, s, k + b * 8, y);
         }
       }
-    }
-    fence_proxy_async_smem();  // the tensor core reads shared memory through the asynchronous proxy
-    asm volatile("bar.sync 1, %0;" ::"n"(kMakers) : "memory");
-
-    if (warp == 1) {
-      // ------------------------------ MMA issuer ------------------------------
-      // The whole warp runs the loop (warp-uniform state); one elected lane issues.
-      const bool issuer = elect_one();
-      tc_fence_after_sync();
-      if (issuer) {
-        for (int i = 0; i < (st1 - st0) * kAtoms; ++i)
-          tc_cp_32x128b_warpx4(tmem + a.t_sx + 4 * i, sdesc_sf_atom(smem_u32(s_sx + i * kSfAtom)));
+      uint8_t byte;
+      // The block's (NVFP4: its half's) largest magnitude; NaN and infinities win.
+      unsigned top = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(y[i]) & 0x7FFFFFFFu);
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      if constexpr (!kNv) top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const bool finite = top < 0x7F800000u;
+      int e = digit_exponent(__uint_as_float(finite ? top : 0u));
+      if constexpr (kNv) {
+        const int e_tok = digit_exponent(__uint_as_float(s_amax[s]));
+        e = max(e, e_tok - 17);
+        const int E = e - e_tok + 8;  // -9 .. 8: the E4M3 power of two
+        byte = (uint8_t)(!finite ? 0x7F : E >= -6 ? (E + 7) << 3 : 1 << (E + 9));
+      } else {
+        byte = (uint8_t)(finite ? e + 127 : 255);
       }
+      // Fixed point: adding 1.5 * 2^23 leaves the rounded integer (at most 2^22) in the low bits, and four
+      // of every digit make the digits -4 .. 3 the fields 0 .. 7.
+      constexpr uint32_t kFours = 04444444444u & ((1u << (3 * kParts)) - 1);
+      const float inv = e8m0_value((uint32_t)max(127 - e, 0));
+      constexpr float kUnit = (float)(1 << (3 * (kParts - 1)));
+      uint32_t v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        v[i] = __float_as_uint(fmaf(finite ? y[i] * inv : 0.0f, kUnit, 12582912.0f)) + (kFours - 0x4B400000u);
+      // Two numbers to a register: the last five digits (15 bits), and of eight the first four.
+      constexpr int kLow = kParts == 5 ? 5 : 4;
+      uint32_t low[4], high[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        low[i] = __byte_perm(v[2 * i], v[2 * i + 1], 0x5410);
+        high[i] = __byte_perm(v[2 * i] >> (3 * kLow), v[2 * i + 1] >> (3 * kLow), 0x5410);
+      }
+      const uint32_t turn = blk & 7;
+      uint8_t* dst = s_x + (size_t)(blk >> 3) * (a.n * 128) + b * 4;
+      // Scale byte of column r: four scale columns to a tile, row r % 32, then r / 32, then the scale column.
+      const int col = kNv ? blk * 2 + (b >> 1) : blk;
+      uint8_t* sc = s_sx + (col >> 2) * kSfAtom + (col & 3);
+      const bool writes_scale = live && (kNv ? (b & 1) == 0 : b == 0);
+      for_digits<kParts>([&](auto p_tag) {
+        constexpr int kP = decltype(p_tag)::value;
+        const uint32_t r = kP * kSp + s;
+        uint32_t w;
+        if constexpr (kParts - kP <= kLow)
+          w = digit_codes<3 * (kParts - 1 - kP)>(low);
+        else
+          w = digit_codes<3 * (kParts - 1 - kP - kLow)>(high);
+        if (live) *reinterpret_cast<uint32_t*>(dst + r * 128 + ((turn ^ (r & 7)) << 4)) = w;
+        if (writes_scale) sc[(r & 31) * 16 + (r >> 5) * 4] = byte;
+      });
+      fence_proxy_async_smem();  // the tensor core reads shared memory through the asynchronous proxy
       __syncwarp();
-      int s = 0, it = 0;
-      uint32_t ph = 0;
-      bool ok = true;
-      for (int tile = cluster; tile < a.tiles && ok; tile += clusters, ++it) {
-        const int buf = it & 1;
-        if (!mbar_wait_warp(&acc_empty[buf], ((it >> 1) & 1) ^ 1)) {
-          if (issuer) set_error(a.err, kErrDrainTimeout);
-          break;
-        }
-        tc_fence_after_sync();
-        const uint32_t t_acc = tmem + buf * a.acc_stride;
-        for (int st = st0; st < st1; ++st) {
-          if (!mbar_wait_warp(&full[s], ph)) {
-            if (issuer) set_error(a.err, kErrDataTimeout);
-            ok = false;
-            break;
-          }
-          tc_fence_after_sync();
-          if (issuer) {
-            const int nmma = min(4, (a.N - st * kStageK) >> 6);
-            const int atoms = kNv ? nmma : (nmma + 1) >> 1;
-            const uint64_t dsw = sdesc_sf_atom(smem_u32(s_sw + s * kSfBytes));
-            const uint32_t tsw = tmem + a.t_sw + s * (4 * kAtoms);
-            const uint32_t tsx = tmem + a.t_sx + (st - st0) * (4 * kAtoms);
-            // Copies and MMAs of one thread run in order.
-            for (int i = 0; i < atoms; ++i) tc_cp_32x128b_warpx4(tsw + 4 * i, dsw + (uint64_t)(i * (kSfAtom >> 4)));
-            const uint64_t dw = sdesc_kmajor_sw128(smem_u32(s_w + s * kStageBytes));
-            const uint64_t dx = sdesc_kmajor_sw128(smem_u32(s_x + (size_t)(st - st0) * (a.n * 128)));
-            for (int j = 0; j < nmma; ++j) {
-              const uint32_t acc = (st > st0 || j > 0) ? 1u : 0u;
-              if constexpr (kNv)
-                tc_mma_nvf4(t_acc, dw + (uint64_t)(j * 2), dx + (uint64_t)(j * 2), idesc_nvf4(kRows, a.n), tsw + 4 * j,
-                            tsx + 4 * j, acc);
-              else
-                tc_mma_mxf4(t_acc, dw + (uint64_t)(j * 2), dx + (uint64_t)(j * 2),
-                            idesc_mxf4(a.n, (2 * j) & 3, (2 * j) & 3), tsw + 4 * (j >> 1), tsx + 4 * (j >> 1), acc);
-            }
-            tc_commit(&empty[s]);
-            if (st == st1 - 1) tc_commit(&acc_full[buf]);
-          }
-          __syncwarp();
-          if (++s == a.ring) {
-            s = 0;
-            ph ^= 1;
-          }
-        }
-      }
-    } else if (warp < 6) {
+      if (lane == 0) mbar_arrive(&made[pass]);
+    }
+
+    if (warp < 4) {
       // ------------------------------ epilogue ------------------------------
       const int quad = warp & 3;  // TMEM lanes 32 quad ..
       float alpha = 1.0f;
       if constexpr (kNv) alpha = a.gs != nullptr ? 1.0f / *a.gs : 1.0f;
+      asm volatile("bar.sync 2, 128;" ::: "memory");  // s_xf is written
       float unit[kSp];
 #pragma unroll
       for (int s = 0; s < kSp; ++s) unit[s] = kNv ? s_xf[s] : 1.0f;
@@ -418,16 +464,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after_sync();
         const uint32_t taddr = tmem + buf * a.acc_stride + ((uint32_t)(32 * quad) << 16);
         float sum[kSp];
-        float f = 1.0f;
-        for (int p = 0; p < a.parts; ++p) {
-          uint32_t v[kSp];
-          tmem_ld_cols<kSp>(taddr + p * kSp, v);
+        // The least digits first: the sum in units of the digit at hand, brought to the next one's.
+        constexpr int kPiece = kSp < 8 ? kSp : 8;  // tokens at a time (registers)
+#pragma unroll
+        for (int s0 = 0; s0 < kSp; s0 += kPiece) {
+          uint32_t v[kParts][kPiece];
+#pragma unroll
+          for (int p = 0; p < kParts; ++p) tmem_ld_cols<kPiece>(taddr + p * kSp + s0, v[p]);
           tmem_ld_wait();
 #pragma unroll
-          for (int s = 0; s < kSp; ++s) asm volatile("" : "+r"(v[s]));  // not used ahead of the wait
+          for (int p = 0; p < kParts; ++p)
 #pragma unroll
-          for (int s = 0; s < kSp; ++s) sum[s] = p == 0 ? __uint_as_float(v[s]) : fmaf(__uint_as_float(v[s]), f, sum[s]);
-          f *= p == 0 ? 0.25f : 0.125f;
+            for (int s = 0; s < kPiece; ++s) asm volatile("" : "+r"(v[p][s]));  // not used ahead of the wait
+#pragma unroll
+          for (int s = 0; s < kPiece; ++s) {
+            sum[s0 + s] = __uint_as_float(v[kParts - 1][s]);
+#pragma unroll
+            for (int p = kParts - 2; p >= 0; --p)
+              sum[s0 + s] = fmaf(sum[s0 + s], 0.125f, __uint_as_float(v[p][s]));
+          }
         }
         tc_fence_before_sync();
         __syncwarp();
@@ -476,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before_sync();
   __syncthreads();
   if (csize > 1) cluster_sync_all();  // peers may still read this CTA's sums
-  if (warp == 1) {
+  if (warp == kMmaWarp) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, 512);
   }
@@ -491,7 +546,7 @@ bool plan(W4Args& a, int sp, int csize, size_t* smem) {
   a.max_stages = (a.stages + csize - 1) / csize;
   a.n = (a.parts * sp + 15) & ~15;
   const size_t fixed = (size_t)a.max_stages * (a.n * 128 + kAtoms * kSfAtom) + 2 * (size_t)kRows * sp * 4 + 32 * 4 +
-                       (2 * kMaxRing + 6) * 8 + 16 + 1024;
+                       (2 * kMaxRing + 6 + kMaxPasses) * 8 + 16 + 1024;
   a.acc_stride = (a.n + 31) & ~31;
   a.t_sx = 2 * a.acc_stride;
   a.t_sw = a.t_sx + a.max_stages * 4 * kAtoms;
@@ -502,22 +557,13 @@ bool plan(W4Args& a, int sp, int csize, size_t* smem) {
   return a.ring >= 3;
 }
 
-template <int kSp, bool kNv>
+template <int kSp, bool kNv, int kParts>
 cudaError_t launch_cfg(const LinearW4A16Launch& L, W4Args& a, cudaStream_t stream) {
-  // Cluster size along K: until the digits fit beside a ring of three stages; then, with fewer tiles
-  // than half of the SMs, while more SMs can take part with two stages or more each.
-  size_t smem = 0;
-  int csize = 1;
-  while (csize <= 8 && !plan<kNv>(a, kSp, csize, &smem)) ++csize;
-  if (csize > 8) return cudaErrorInvalidConfiguration;
-  while (csize * 2 <= 8 && a.tiles * csize * 2 <= sm_count() && a.stages >= csize * 4) csize *= 2;
-  if (!plan<kNv>(a, kSp, csize, &smem)) return cudaErrorInvalidConfiguration;
-
   CUtensorMap tm;
   if (!make_map_2d(&tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, L.w_codes, (uint64_t)L.N / 2, (uint64_t)L.M, (uint64_t)L.N / 2,
                    kStageK / 2, kRows, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
-  auto kern = k_linear_w4a16<kSp, kNv>;
+  auto kern = k_linear_w4a16<kSp, kNv, kParts>;
   static bool attr_set[64] = {false};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
@@ -528,34 +574,56 @@ cudaError_t launch_cfg(const LinearW4A16Launch& L, W4Args& a, cudaStream_t strea
   }
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)csize;
+  attr[1].val.clusterDim.x = 1;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  // As many clusters as run at the same time (clusters do not cross GPCs, so fewer than SMs / size).
-  int clusters = sm_count();
-  if (csize > 1) {
-    static int active[64][9] = {};
-    if (active[dev][csize] == 0) {
-      cfg.gridDim = dim3((unsigned)csize);
-      cudaLaunchConfig_t one = cfg;
-      one.dynamicSmemBytes = kSmemLimit;
-      int n = 0;
-      cudaError_t e = cudaOccupancyMaxActiveClusters(&n, kern, &one);
-      if (e != cudaSuccess) return e;
-      active[dev][csize] = n < 1 ? 1 : n;
+  // Cluster size along K, by the time that it would take (us; fitted to sizes 1 to 8 for 1 to 16 tokens,
+  // K = 4096 and 12288, 4096 to 24576 out-features):
+  //   * rounds of tiles over the clusters that run at the same time (clusters do not cross GPCs), each
+  //     0.37 per stage with every SM streaming, or 0.5 per CTA that exchanges sums where that is longer;
+  //   * the digits, 0.007 per stage, token and digit, which the CTAs of a cluster share;
+  //   * 1 for a cluster's start.
+  // Four tokens x 4096 x 24576: 17.1 us alone, 14.9 in pairs, 19.0 in threes; one x 4096 x 4096 (32
+  // tiles): 9.3 in pairs, 7.2 in fours, 10.7 in eights; one x 4096 x 18944 (one tile per SM): 11.3 alone,
+  // 12.4 in pairs.
+  static int active[64][9] = {};
+  int csize = 0;
+  size_t smem = 0;
+  float best = 0.0f;
+  for (int c = 1; c <= 8 && c <= a.stages; ++c) {
+    if (!plan<kNv>(a, kSp, c, &smem)) continue;
+    if (active[dev][c] == 0) {
+      int n = sm_count();
+      if (c > 1) {
+        attr[1].val.clusterDim.x = (unsigned)c;
+        cfg.gridDim = dim3((unsigned)c);
+        cfg.dynamicSmemBytes = kSmemLimit;
+        const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+        if (e != cudaSuccess) return e;
+      }
+      active[dev][c] = n < 1 ? 1 : n;
     }
-    clusters = active[dev][csize];
+    const int rounds = (a.tiles + active[dev][c] - 1) / active[dev][c];
+    const float round = 0.37f * a.max_stages;
+    const float t = rounds * (c > 1 && round < 0.5f * c ? 0.5f * c : round) + 0.007f * a.max_stages * a.S * kParts +
+                    (c > 1 ? 1.0f : 0.0f);
+    if (csize == 0 || t < best) {
+      csize = c;
+      best = t;
+    }
   }
-  if (clusters > a.tiles) clusters = a.tiles;
+  if (csize == 0 || !plan<kNv>(a, kSp, csize, &smem)) return cudaErrorInvalidConfiguration;
+  const int clusters = a.tiles < active[dev][csize] ? a.tiles : active[dev][csize];
+  attr[1].val.clusterDim.x = (unsigned)csize;
   cfg.gridDim = dim3((unsigned)(clusters * csize));
+  cfg.dynamicSmemBytes = smem;
   return cudaLaunchKernelEx(&cfg, kern, tm, a);
 }
 
@@ -582,7 +650,7 @@ cudaError_t launch_fmt(const LinearW4A16Launch& L, cudaStream_t stream) {
   a.err = L.err;
   a.tiles = (L.M + kRows - 1) / kRows;
   a.stages = (L.N + kStageK - 1) / kStageK;
-  a.parts = L.out_bf16 ? 5 : kMaxParts;
+  a.parts = L.out_bf16 ? kPartsBf16 : kPartsF32;
   auto padded = [](int s) { return s <= 1 ? 1 : s <= 2 ? 2 : s <= 4 ? 4 : s <= 8 ? 8 : 16; };
   // Tokens per launch: as many as eight CTAs hold the digits of.
   int per = L.S;
@@ -600,11 +668,11 @@ cudaError_t launch_fmt(const LinearW4A16Launch& L, cudaStream_t stream) {
     a.out = static_cast<uint8_t*>(L.out) + (size_t)s0 * L.ldo * (L.out_bf16 ? 2 : 4);
     cudaError_t e = cudaErrorInvalidConfiguration;
     switch (padded(a.S)) {
-      case 1: e = launch_cfg<1, kNv>(L, a, stream); break;
-      case 2: e = launch_cfg<2, kNv>(L, a, stream); break;
-      case 4: e = launch_cfg<4, kNv>(L, a, stream); break;
-      case 8: e = launch_cfg<8, kNv>(L, a, stream); break;
-      case 16: e = launch_cfg<16, kNv>(L, a, stream); break;
+      case 1: e = L.out_bf16 ? launch_cfg<1, kNv, kPartsBf16>(L, a, stream) : launch_cfg<1, kNv, kPartsF32>(L, a, stream); break;
+      case 2: e = L.out_bf16 ? launch_cfg<2, kNv, kPartsBf16>(L, a, stream) : launch_cfg<2, kNv, kPartsF32>(L, a, stream); break;
+      case 4: e = L.out_bf16 ? launch_cfg<4, kNv, kPartsBf16>(L, a, stream) : launch_cfg<4, kNv, kPartsF32>(L, a, stream); break;
+      case 8: e = L.out_bf16 ? launch_cfg<8, kNv, kPartsBf16>(L, a, stream) : launch_cfg<8, kNv, kPartsF32>(L, a, stream); break;
+      case 16: e = L.out_bf16 ? launch_cfg<16, kNv, kPartsBf16>(L, a, stream) : launch_cfg<16, kNv, kPartsF32>(L, a, stream); break;
     }
     if (e != cudaSuccess) return e;
   }

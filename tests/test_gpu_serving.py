@@ -49,18 +49,18 @@ def w4a16_check(out, x, A, B, codes, lin, fmt, gs=1.0):
     y, cond = R.transform(xd, A, B) if A is not None else (xd, np.abs(xd))
     w = R.weights(codes, lin, fmt)
     ref = y @ w.T / gs
-    # fp32 transform (12 roundings, half a step each).  y is a sum of E2M1 digits under its scale group's 2^e, with
-    # |y| <= 6 * 2^e and, e being the smallest such, max |y| > 3 * 2^e: the first digit leaves at most 1, every
-    # further one at most 1/2 of a unit that shrinks by 4, then 8 each, so P digits leave 2^e / (8 * 8^(P - 2)): 2^-12 2^e
-    # of five (bf16 out), 2^-21 2^e of eight, and a third of that relative to the largest.  NVFP4's e is at least 2^-17 of
-    # a bound of the token's largest value, which is at most 4 |A|_1 |B|_1 (here below 2^5) above it.
+    # fp32 transform (12 roundings, half a step each).  y is rounded to a fixed-point number under its scale group's 2^e,
+    # 2^e <= max |y|: half a step of 8^-4 2^e (bf16 out), or 8^-7 2^e, so 2^-13 or 2^-22 of the group's largest.  NVFP4's
+    # 2^e is at least 2^-17 of that of a bound of the token's largest value, which lies at most 4 |A|_1 |B|_1 (here below
+    # 2^5) above it: 2^-25 and 2^-34 of the largest.
     fine = out.dtype != BF
     G = 32 if fmt == "mxfp4" else 16
     top = np.repeat(np.abs(y).reshape(len(y), -1, G).max(2), G, axis=1)
     each = cond * (12 * 2.0 ** -24) + top * (2.0 ** -22 if fine else 2.0 ** -13)
     if fmt == "nvfp4":
         each = each + np.abs(y).max(1, keepdims=True) * (2.0 ** -33 if fine else 2.0 ** -24)
-    # and one fp32 rounding (two half steps: the tensor core truncates) per 64 products, digits adding up to 2 |y|
+    # and one fp32 rounding (two half steps: the tensor core truncates) per 64 products, the digits' values adding
+    # up to 2 |y| and their remainders
     tol = (each + np.abs(y) * ((N / 8 + 24) * 2.0 ** -23)) @ np.abs(w).T / gs
     tol += np.abs(ref) * (2.0 ** -8 if out.dtype == BF else 2.0 ** -23)
     err = np.abs(host(out) - ref)
