@@ -9,14 +9,15 @@
 // group of 300 rows would cost 512, here 304.  The groups' tokens are split evenly over their tiles.
 //
 // The roles and the pipeline are those of the pair GEMM for one matrix (gemm_pair.cu): warp 0 loads
-// codes and weight scales by TMA into three 70 KB stages of K = 512, warp 10 of the leader copies
-// the scales into TMEM, warp 1 issues the MMAs, eight epilogue warps drain the accumulator.  What is
-// different is the token side's scales: a group starts at any row, while the tensor cores want
-// 128-row x 4-column tiles, so they come in the LINEAR layout and three warps per CTA (one per ring
-// slot) re-tile them: each lane reads the 16 scale bytes of rows l, l + 32, .. of the tile and writes
-// the tiles with one 16-byte store per atom.  The leader's copies read both CTAs' shared memory, so
-// the peer's warps publish theirs with a cluster-scope release; that arrive is slow (about 1 us while
-// operand loads are in flight), which three warps hide as the loads' own latency is hidden.
+// codes and weight scales by TMA into three 66 KB stages of K = 512, warp 10 of the leader copies the
+// scales into TMEM, warp 1 issues the MMAs, eight epilogue warps drain the accumulator.  What is
+// different is the token side's scales: a group starts at any row, while the tensor cores want 128-row
+// x 4-column tiles, so they come in the LINEAR layout and three warps per CTA re-tile them: each lane
+// reads the 16 scale bytes of rows l, l + 32, .. of the tile and writes the tiles with one 16-byte
+// store per atom.  The leader's copies read both CTAs' shared memory, so the peer's warps publish theirs
+// with a cluster-scope release, which takes about as long as the operand loads in flight; the scales
+// therefore have a ring of their own and run up to five stages ahead.  (In the stages' ring, 16384
+// rows of 8 experts took 169 us.)
 //
 // Epilogue: a lane holds one weight row, a register one token; pairs of tokens are exchanged between
 // neighbouring lanes so that a store writes two consecutive out-features of one token (64
@@ -42,15 +43,19 @@ constexpr int kSfAtom = 512;
 constexpr int kAtoms = 4;               // 4-scale atoms per row and stage
 constexpr int kSfwBytes = kAtoms * kSfAtom;
 constexpr int kSfxBytes = 2 * kAtoms * kSfAtom;
-constexpr int kStageBytes = kWBytes + kXBytes + kSfwBytes + kSfxBytes;
+constexpr int kStageBytes = kWBytes + kXBytes + kSfwBytes;
+constexpr int kSxSlots = 5;             // ring of the token scales, made up to five stages ahead
 constexpr int kEpiWarps = 8;
 constexpr int kSfWarp = 2 + kEpiWarps;
-constexpr int kSxWarp = kSfWarp + 1;    // three warps, one per stage slot
-constexpr int kThreads = (kSxWarp + kStages) * 32;
+constexpr int kSxWarp = kSfWarp + 1;    // first of the warps that re-tile the token scales
+constexpr int kSxWarps = 3;
+constexpr int kThreads = (kSxWarp + kSxWarps) * 32;
 constexpr int kTmemCols = 512;
 constexpr int kSfwCols = 4 * kAtoms, kSfxCols = 8 * kAtoms;
 constexpr int kListBytes = (3 * kMaxExperts + 4) * 4;  // per expert: first row, rows, first tile
-constexpr int kBarOffset = kStages * kStageBytes + kListBytes;
+constexpr int kSxOffset = kStages * kStageBytes;
+constexpr int kListOffset = kSxOffset + kSxSlots * kSfxBytes;
+constexpr int kBarOffset = kListOffset + kListBytes;
 constexpr int kSmemBytes = kBarOffset + 256 + 1024;
 static_assert(kStageBytes % 1024 == 0 && kListBytes % 16 == 0, "alignment");
 static_assert(kTileN + kStages * (kSfwCols + kSfxCols) <= kTmemCols, "TMEM budget");
@@ -133,14 +138,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   // (an offset, so that the compiler still knows these for shared addresses)
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  int* s_off = reinterpret_cast<int*>(smem + kStages * kStageBytes);  // [E] {first row, rows}
+  int* s_off = reinterpret_cast<int*>(smem + kListOffset);             // [E] {first row, rows}
   int* s_unit = s_off + 2 * kMaxExperts;                              // [E + 1] first tile of each expert
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kBarOffset);
   uint64_t* empty = full + kStages;
   uint64_t* acc_full = empty + kStages;
   uint64_t* acc_empty = acc_full + 1;
   uint64_t* sf_ready = acc_empty + 1;  // [kStages], leader only
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sf_ready + kStages);
+  uint64_t* sx_full = sf_ready + kStages;  // [kSxSlots], leader only
+  uint64_t* sx_empty = sx_full + kSxSlots;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sx_empty + kSxSlots);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -152,9 +159,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tma_prefetch_map(&tm_x8);
     tma_prefetch_map(&tm_x32);
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&full[s], 3);  // the leader's expect_tx, and the token scales of both CTAs
+      mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
       mbar_init(&sf_ready[s], 1);
+    }
+    for (int s = 0; s < kSxSlots; ++s) {
+      mbar_init(&sx_full[s], 2);  // both CTAs' token scales
+      mbar_init(&sx_empty[s], 1);
     }
     mbar_init(acc_full, 1);
     mbar_init(acc_empty, 2 * kEpiWarps);
@@ -251,18 +262,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp >= kSxWarp) {
-    // ---------------------- token scales (both CTAs): slot = warp - kSxWarp ----------------------
-    const int slot = warp - kSxWarp;
-    uint8_t* dst = smem + slot * kStageBytes + kWBytes + kXBytes + kSfwBytes;
-    const uint32_t bar = mapa_shared(smem_u32(&full[slot]), 0);
-    int stage = 0;          // running stage number; this warp's are those with stage % kStages == slot
-    uint32_t ph = 0;
+    // ---------------------- token scales (both CTAs): every kSxWarps-th stage ----------------------
+    const int turn = warp - kSxWarp;
+    int stage = 0;          // running stage number
     bool ok = true;
     for (int u = cluster_id; u < num_units && ok; u += num_clusters) {
       const Tile t = tile_of(a, s_off, s_unit, u);
       const int groups = (t.n + 31) >> 5;  // 32-row groups
       for (int ks = 0; ks < nks; ++ks, ++stage) {
-        if (stage % kStages != slot) continue;
+        if (stage % kSxWarps != turn) continue;
         const int c0 = ks * 16;
         uint32_t v[8][4];
 #pragma unroll
@@ -286,12 +294,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (!mbar_wait_warp(&empty[slot], ph ^ 1)) {
+        const int slot = stage % kSxSlots;
+        if (!mbar_wait_warp(&sx_empty[slot], ((stage / kSxSlots) & 1) ^ 1)) {
           if (lane == 0) set_error(a.err, kErrReleaseTimeout);
           ok = false;
           break;
         }
-        ph ^= 1;
+        uint8_t* dst = smem + kSxOffset + slot * kSfxBytes;
         // Atom x of the row tile R: row r at 16 (r % 32), its 32-row quarter's four bytes beside each other.
 #pragma unroll
         for (int R = 0; R < 2; ++R)
@@ -302,7 +311,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                   make_uint4(v[4 * R][x], v[4 * R + 1][x], v[4 * R + 2][x], v[4 * R + 3][x]);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive_release_cluster(bar);
+        if (lane == 0) {
+          if (leader)
+            mbar_arrive(&sx_full[slot]);
+          else
+            mbar_arrive_release_cluster(mapa_shared(smem_u32(&sx_full[slot]), 0));
+        }
       }
     }
   } else if (warp == 1) {
@@ -355,13 +369,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ---------------------- scale copies into TMEM (leader only) ----------------------
     if (leader) {
       const bool issuer = elect_one();
-      int s = 0;
-      uint32_t ph = 0;
+      int s = 0, x_slot = 0;
+      uint32_t ph = 0, x_ph = 0;
       bool ok = true;
       for (int u = cluster_id; u < num_units && ok; u += num_clusters) {
         const int n = tile_of(a, s_off, s_unit, u).n;
         for (int ks = 0; ks < nks; ++ks) {
-          if (!mbar_wait_warp_cluster(&full[s], ph)) {
+          if (!mbar_wait_warp_cluster(&sx_full[x_slot], x_ph) || !mbar_wait_warp(&full[s], ph)) {
             if (issuer) set_error(a.err, kErrDataTimeout);
             ok = false;
             break;
@@ -370,7 +384,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const int nmma = min(8, (a.N - ks * kBK) >> 6);
           const int atoms = (nmma + 1) >> 1;
           const uint64_t dw = sdesc_sf_atom(smem_u32(smem + s * kStageBytes) + kWBytes + kXBytes);
-          const uint64_t dx = dw + (uint64_t)(kSfwBytes >> 4);
+          const uint64_t dx = sdesc_sf_atom(smem_u32(smem + kSxOffset + x_slot * kSfxBytes));
           const uint32_t tw = t_sfw + s * kSfwCols, tx = t_sfx + s * kSfxCols;
           if (issuer) {
             for (int x = 0; x < atoms; ++x) {
@@ -380,11 +394,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               if (n > 128) tc_cp_pair_32x128b_warpx4(tx + x * 8 + 4, dx + (uint64_t)((kAtoms * kSfAtom) >> 4) + off);
             }
             tc_commit_pair_local(&sf_ready[s]);
+            tc_commit_pair(&sx_empty[x_slot], 0x3);
           }
           __syncwarp();
           if (++s == kStages) {
             s = 0;
             ph ^= 1;
+          }
+          if (++x_slot == kSxSlots) {
+            x_slot = 0;
+            x_ph ^= 1;
           }
         }
       }
@@ -403,11 +422,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         break;
       }
       tc_fence_after_sync();
-      uint32_t v[4][32];
       const uint32_t taddr = t_acc + ((uint32_t)(32 * quad) << 16) + col0;
+      uint32_t v[4][kOutBF16 ? 16 : 32];  // bf16: token pairs
 #pragma unroll
       for (int c = 0; c < 4; ++c)
-        if (32 * c < wcols) tmem_ld_32cols(taddr + 32 * c, v[c]);
+        if (32 * c < wcols) {
+          if constexpr (kOutBF16) {
+            uint32_t w[32];
+            tmem_ld_32cols(taddr + 32 * c, w);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(w[i]));  // not used ahead of the wait
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[c][i] = pack_bf16x2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+          } else {
+            tmem_ld_32cols(taddr + 32 * c, v[c]);
+          }
+        }
       tmem_ld_wait();
       tc_fence_before_sync();
       __syncwarp();
@@ -423,7 +454,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (32 * c >= left) break;
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
-            const uint32_t r = pack_bf16x2(__uint_as_float(v[c][i]), __uint_as_float(v[c][i + 1]));
+            const uint32_t r = v[c][i / 2];
             const uint32_t p = __shfl_xor_sync(0xffffffffu, r, 1);
             const uint32_t w = (lane & 1) ? __byte_perm(p, r, 0x7632) : __byte_perm(r, p, 0x5410);
             if (m_ok && 32 * c + i + (lane & 1) < left)
