@@ -12,7 +12,7 @@
 // codes and weight scales by TMA into three 66 KB stages of K = 512, warp 10 of the leader copies the
 // scales into TMEM, warp 1 issues the MMAs, eight epilogue warps drain the accumulator.  What is
 // different is the token side's scales: a group starts at any row, while the tensor cores want 128-row
-// x 4-column tiles, so they come in the LINEAR layout and three warps per CTA re-tile them: each lane
+// x 4-column tiles, so they come in the LINEAR layout and five warps per CTA re-tile them: each lane
 // reads the 16 scale bytes of rows l, l + 32, .. of the tile and writes the tiles with one 16-byte
 // store per atom.  The leader's copies read both CTAs' shared memory, so the peer's warps publish theirs
 // with a cluster-scope release, which takes about as long as the operand loads in flight; the scales
@@ -48,7 +48,7 @@ constexpr int kSxSlots = 5;             // ring of the token scales, made up to 
 constexpr int kEpiWarps = 8;
 constexpr int kSfWarp = 2 + kEpiWarps;
 constexpr int kSxWarp = kSfWarp + 1;    // first of the warps that re-tile the token scales
-constexpr int kSxWarps = 3;
+constexpr int kSxWarps = 5;
 constexpr int kThreads = (kSxWarp + kSxWarps) * 32;
 constexpr int kTmemCols = 512;
 constexpr int kSfwCols = 4 * kAtoms, kSfxCols = 8 * kAtoms;
@@ -423,11 +423,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       tc_fence_after_sync();
       const uint32_t taddr = t_acc + ((uint32_t)(32 * quad) << 16) + col0;
-      uint32_t v[4][kOutBF16 ? 16 : 32];  // bf16: token pairs
+      const int m = t.w_row + (int)rank * kRowsPerCta + 32 * quad + lane;
+      const bool m_ok = m < a.M;  // M is a multiple of 16: neighbouring lanes agree
+      const int left = min(t.count - col0, wcols);
+      auto release = [&]() {
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(acc_empty_leader);
+      };
+      // (16 warps have 128 registers each: bf16 holds all of its 128 columns as pairs, fp32 64 at a time.)
+      if constexpr (kOutBF16) {
+        uint32_t v[4][16];
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (32 * c < wcols) {
-          if constexpr (kOutBF16) {
+        for (int c = 0; c < 4; ++c)
+          if (32 * c < wcols) {
             uint32_t w[32];
             tmem_ld_32cols(taddr + 32 * c, w);
             tmem_ld_wait();
@@ -435,19 +444,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(w[i]));  // not used ahead of the wait
 #pragma unroll
             for (int i = 0; i < 16; ++i) v[c][i] = pack_bf16x2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
-          } else {
-            tmem_ld_32cols(taddr + 32 * c, v[c]);
           }
-        }
-      tmem_ld_wait();
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(acc_empty_leader);
-
-      const int m = t.w_row + (int)rank * kRowsPerCta + 32 * quad + lane;
-      const bool m_ok = m < a.M;  // M is a multiple of 16: neighbouring lanes agree
-      const int left = min(t.count - col0, wcols);
-      if constexpr (kOutBF16) {
+        release();
         uint16_t* o = static_cast<uint16_t*>(a.out) + (size_t)(t.row + col0 + (lane & 1)) * a.ldo + (m & ~1);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -456,19 +454,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 32; i += 2) {
             const uint32_t r = v[c][i / 2];
             const uint32_t p = __shfl_xor_sync(0xffffffffu, r, 1);
-            const uint32_t w = (lane & 1) ? __byte_perm(p, r, 0x7632) : __byte_perm(r, p, 0x5410);
-            if (m_ok && 32 * c + i + (lane & 1) < left)
-              *reinterpret_cast<uint32_t*>(o + (size_t)(32 * c + i) * a.ldo) = w;
+            const uint32_t x = (lane & 1) ? __byte_perm(p, r, 0x7632) : __byte_perm(r, p, 0x5410);
+            if (m_ok && 32 * c + i + (lane & 1) < left) *reinterpret_cast<uint32_t*>(o + (size_t)(32 * c + i) * a.ldo) = x;
           }
         }
       } else {
         float* o = static_cast<float*>(a.out) + (size_t)(t.row + col0) * a.ldo + m;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (32 * c >= left) break;
+        for (int h = 0; h < 2; ++h) {
+          uint32_t w[2][32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (m_ok && 32 * c + i < left) o[(size_t)(32 * c + i) * a.ldo] = __uint_as_float(v[c][i]);
+          for (int c = 0; c < 2; ++c)
+            if (64 * h + 32 * c < wcols) tmem_ld_32cols(taddr + 64 * h + 32 * c, w[c]);
+          tmem_ld_wait();
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(w[c][i]));
+          if (h == 1) release();
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            if (64 * h + 32 * c >= left) break;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (m_ok && 64 * h + 32 * c + i < left) o[(size_t)(64 * h + 32 * c + i) * a.ldo] = __uint_as_float(w[c][i]);
+          }
         }
       }
     }
