@@ -9,8 +9,11 @@
 // are stored as the E4M3 NaN and take no part in the amax.
 //
 // One CTA owns one block that receives tokens (blockIdx.x: the touched pages of the batch in order;
-// y: kv head; z: K or V), so no block has two writers and the result does not depend on order.  Rows
-// are read twice (amax, then codes); the second read hits L1/L2.
+// y: kv head; z: K or V), so no block has two writers and the result does not depend on order.  Up to
+// eight 8-element chunks per thread (64 rows of 128) are loaded together and stay in registers from the
+// maximum to the codes; larger blocks are read twice, eight chunks at a time, the second time from L2.
+// (One chunk at a time, each with its own trip to memory: 23.7 us for 8000 rows of 8 x 128 instead of
+// 17.1.)
 #include <cstdint>
 
 #include "kernels.h"
@@ -21,6 +24,7 @@ namespace batq {
 namespace {
 
 constexpr int kThreads = 128;
+constexpr int kPiece = 8;  // chunks in flight per thread
 
 // Smallest e >= -127 with |a| <= 448 * 2^e (448 = 1.75 * 2^8), a finite and >= 0.
 __device__ __forceinline__ int block_exponent(float a) {
@@ -33,26 +37,40 @@ __device__ __forceinline__ float finite_or_nan(float v) {
   return fabsf(v) <= 3.402823466e38f ? v : __uint_as_float(0x7FC00000u);
 }
 
-// Eight consecutive elements of a row.
+// Eight consecutive elements of a row, as loaded.
 template <bool kBF16>
-__device__ __forceinline__ void load8(const uint8_t* p, float (&v)[8]) {
+struct Raw8 {
+  uint4 q[kBF16 ? 1 : 2];
+};
+template <bool kBF16>
+__device__ __forceinline__ Raw8<kBF16> load8(const uint8_t* p) {
+  Raw8<kBF16> r;
+#pragma unroll
+  for (int i = 0; i < (kBF16 ? 1 : 2); ++i) r.q[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+  return r;
+}
+template <bool kBF16>
+__device__ __forceinline__ void values8(const Raw8<kBF16>& r, float (&v)[8]) {
   if constexpr (kBF16) {
-    const uint4 q = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    const uint32_t w[4] = {r.q[0].x, r.q[0].y, r.q[0].z, r.q[0].w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       v[2 * i] = __uint_as_float(w[i] << 16);
       v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
     }
   } else {
-    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 16);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      v[4 * i] = __uint_as_float(r.q[i].x);
+      v[4 * i + 1] = __uint_as_float(r.q[i].y);
+      v[4 * i + 2] = __uint_as_float(r.q[i].z);
+      v[4 * i + 3] = __uint_as_float(r.q[i].w);
+    }
   }
 }
 
 template <bool kBF16>
-__global__ void __launch_bounds__(kThreads) k_kv8_append(const Kv8AppendLaunch a) {
+__global__ void __launch_bounds__(kThreads, kBF16 ? 9 : 5) k_kv8_append(const Kv8AppendLaunch a) {
   __shared__ int s_seq, s_page;
   __shared__ float s_amax[kThreads / 32];
   griddep_wait();
@@ -96,8 +114,7 @@ __global__ void __launch_bounds__(kThreads) k_kv8_append(const Kv8AppendLaunch a
   __syncthreads();
   const int b = s_seq;
   if (b < 0) return;
-  const int pid = a.page_table[(size_t)b * a.max_pages + s_page];
-  if (pid < 0 || pid >= a.num_pages) return;
+  const int pid = a.page_table[(size_t)b * a.max_pages + s_page];  // (checked once the rows are on their way)
   const SeqRows s = seq_rows(a.cu_new, a.seq_lens, b, a.T, max_len);
   const int pos0 = a.seq_lens[b] - s.count;                      // position of the sequence's first new token
   const int begin = max(pos0, s_page * a.page_size);             // this page's new positions
@@ -110,24 +127,41 @@ __global__ void __launch_bounds__(kThreads) k_kv8_append(const Kv8AppendLaunch a
   const size_t ld = (size_t)(is_v ? a.ldv : a.ldk) * esz;
   const uint8_t* x = static_cast<const uint8_t*>(is_v ? a.V : a.K) + (size_t)(s.begin + begin - pos0) * ld +
                      (size_t)h * D * esz;
+  // Chunk c: row c / per_row of the new ones, elements 8 (c % per_row) ..; per_row is a power of two.
+  const int row_shift = 31 - __clz(per_row);
+  auto load_piece = [&](int c0, Raw8<kBF16> (&raw)[kPiece]) {
+#pragma unroll
+    for (int j = 0; j < kPiece; ++j) {
+      const int c = c0 + j * kThreads;
+      if (c < chunks) raw[j] = load8<kBF16>(x + (size_t)(c >> row_shift) * ld + (size_t)(c & (per_row - 1)) * 8 * esz);
+    }
+  };
+  Raw8<kBF16> raw[kPiece];
+  load_piece(tid, raw);
+  if (pid < 0 || pid >= a.num_pages) return;
   const size_t block = (size_t)pid * a.kv_heads + h;
   uint8_t* codes = (is_v ? a.v_codes : a.k_codes) + block * ((size_t)a.page_size * D);
   uint8_t* scale = (is_v ? a.v_scales : a.k_scales) + block;
-
+  const int e_old = off0 > 0 ? (int)*scale - 127 : -127;
   float amax = 0.0f;
-  for (int c = tid; c < chunks; c += kThreads) {
-    float v[8];
-    load8<kBF16>(x + (size_t)(c / per_row) * ld + (size_t)(c % per_row) * 8 * esz, v);
+  for (int c0 = tid; c0 < chunks; c0 += kPiece * kThreads) {
+    if (c0 != tid) load_piece(c0, raw);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float m = fabsf(v[i]);
-      amax = m <= 3.402823466e38f ? fmaxf(amax, m) : amax;
+    for (int j = 0; j < kPiece; ++j) {
+      if (c0 + j * kThreads < chunks) {
+        float v[8];
+        values8<kBF16>(raw[j], v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float m = fabsf(v[i]);
+          amax = m <= 3.402823466e38f ? fmaxf(amax, m) : amax;
+        }
+      }
     }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   if (lane == 0) s_amax[tid >> 5] = amax;
-  const int e_old = off0 > 0 ? (int)*scale - 127 : -127;
   __syncthreads();  // also: every thread has the old scale before it is replaced
   amax = s_amax[0];
 #pragma unroll
@@ -152,12 +186,19 @@ __global__ void __launch_bounds__(kThreads) k_kv8_append(const Kv8AppendLaunch a
   }
   const float inv = e8m0_value((uint32_t)max(127 - e, 0));  // 2^-e
   uint8_t* dst = codes + (size_t)off0 * D;
-  for (int c = tid; c < chunks; c += kThreads) {
-    float v[8];
-    load8<kBF16>(x + (size_t)(c / per_row) * ld + (size_t)(c % per_row) * 8 * esz, v);
+  for (int c0 = tid; c0 < chunks; c0 += kPiece * kThreads) {
+    if (chunks > kPiece * kThreads) load_piece(c0, raw);  // otherwise still there
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = finite_or_nan(v[i]) * inv;
-    reinterpret_cast<uint2*>(dst)[c] = make_uint2(e4m3x4(v[0], v[1], v[2], v[3]), e4m3x4(v[4], v[5], v[6], v[7]));
+    for (int j = 0; j < kPiece; ++j) {
+      const int c = c0 + j * kThreads;
+      if (c < chunks) {
+        float v[8];
+        values8<kBF16>(raw[j], v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = finite_or_nan(v[i]) * inv;
+        reinterpret_cast<uint2*>(dst)[c] = make_uint2(e4m3x4(v[0], v[1], v[2], v[3]), e4m3x4(v[4], v[5], v[6], v[7]));
+      }
+    }
   }
 }
 
