@@ -535,134 +535,49 @@ def batq_rmsnorm_linear(X, gamma, eps, A, B, ratios, w_codes, w_scales, M, works
 
 # ------------------------------------------------------------ serving operators
 #
-# These calls run many times per generated token, so their checks are few plain attribute reads per
-# tensor (a decode step's kernels take about as long as one call of the helpers above).
+# These calls run many times per generated token, and their kernels take a few microseconds, so the
+# compiled module _serving (binding/serving.cpp) reads and checks their tensors.  A tensor that is not
+# on the current device, not contiguous where it has to be, or of another shape or type raises
+# ValueError (TypeError: no tensor); other refusals raise BatqError with the library's status.
 
-class _Torch:
-    """What the serving calls use of torch, looked up once."""
-
-    def __init__(self):
-        torch = _torch()
-        self.u8, self.i32, self.f32 = torch.uint8, torch.int32, torch.float32
-        self.codes = {torch.bfloat16: BATQ_BF16, torch.float32: BATQ_F32}
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        self.device = torch.cuda.current_device
-        self.raw_stream = raw or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-        self.lib = _lib.load()
+_SERVING = None
+_CONVERT = -1  # _serving's answer where A is not a contiguous fp32 array
 
 
-_T = None
+def _load_serving():
+    global _SERVING
+    if _SERVING is None:
+        _torch()
+        _lib.load()
+        try:
+            from . import _serving
+        except ImportError as e:
+            raise RuntimeError("_serving.so is missing or does not load: build it with "
+                               "`python -m mxfp4_w4a4_post_block_b200.build`") from e
+        _SERVING = _serving
+    return _SERVING
 
 
-def _serving(stream):
-    """(torch names, current device, raw stream) of a call."""
-    global _T
-    if _T is None:
-        _T = _Torch()
-    dev = _T.device()
-    if stream is None:
-        return _T, dev, _T.raw_stream(dev)
-    return _T, dev, stream if isinstance(stream, int) else stream.cuda_stream
-
-
-def _array(t, dtype, dev, name, numel=0):
-    """Pointer of a contiguous tensor of `dtype` on the current device, of `numel` elements at least."""
-    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous() or t.numel() < numel:
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor on cuda:{dev} (the current device) of at least "
-                         f"{numel} elements, got {t.dtype}, {tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
-
-
-def _matrix(T, t, cols, dev, name):
-    """(pointer, dtype code, rows, row stride) of a bf16 or fp32 matrix whose rows hold `cols` consecutive elements."""
-    code = T.codes.get(t.dtype)
-    shape, stride = t.shape, t.stride()
-    if code is None or t.get_device() != dev or len(shape) != 2 or shape[1] != cols or stride[1] != 1:
-        raise ValueError(f"{name} must be a bf16 or fp32 matrix of rows of {cols} consecutive elements on cuda:{dev} (the "
-                         f"current device), got {t.dtype}, {tuple(shape)} on {t.device}")
-    rows = shape[0]
-    return t.data_ptr(), code, rows, stride[0] if rows > 1 else max(stride[0], cols)
-
-
-def _factor(a, count, name):
-    """Host floats: (address, the array that holds them)."""
-    if type(a) is not np.ndarray or a.dtype != np.float32 or a.size != count or not a.flags.c_contiguous:
-        a = _host_f32(a, count, name)
-    return a.__array_interface__["data"][0], a
-
-
-def _status(status, call):
-    if status:
-        raise BatqError(status, call)
-
-
-def _batch(T, cu, seq_lens, page_table, rows, dev, cu_name):
-    """(cu, lens, table, batch, max_pages) of a ragged batch's arrays."""
-    B = seq_lens.numel()
-    shape = page_table.shape
-    if len(shape) != 2 or shape[0] != B:
-        raise ValueError("page_table must be batch x max_pages")
-    if cu is None:
-        if rows < B:
-            raise ValueError(f"without {cu_name} there must be a row for each sequence")
-    elif cu.numel() != B + 1:
-        raise ValueError(f"{cu_name} must hold batch + 1 entries")
-    return (None if cu is None else _array(cu, T.i32, dev, cu_name), _array(seq_lens, T.i32, dev, "seq_lens"),
-            _array(page_table, T.i32, dev, "page_table"), B, shape[1])
-
-
-def _kv8_cache(T, k_codes, k_scales, v_codes, v_scales, dev):
-    """(pointers, num_pages, kv_heads, page_size, head_dim) of a cache, after checking its four tensors."""
-    shape = k_codes.shape
-    if len(shape) != 4 or v_codes.shape != shape:
-        raise ValueError("cache codes must be num_pages x kv_heads x page_size x head_dim, the same for K and V")
-    P, H, page, D = shape
-    if k_scales.shape != (P, H) or v_scales.shape != (P, H):
-        raise ValueError("k_scales and v_scales must be num_pages x kv_heads")
-    return ((_array(k_codes, T.u8, dev, "k_codes"), _array(k_scales, T.u8, dev, "k_scales"),
-             _array(v_codes, T.u8, dev, "v_codes"), _array(v_scales, T.u8, dev, "v_scales")), P, H, page, D)
-
-
-def _bytes(t, dev, name):
-    """(pointer, bytes) of a contiguous device buffer of any type."""
-    if t.get_device() != dev or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous tensor on cuda:{dev} (the current device)")
-    return t.data_ptr(), t.numel() * t.element_size()
-
-
-def _mma_scale_bytes(M, columns):
-    return (M + 127) // 128 * 128 * ((columns + 3) // 4 * 4)
+def _raw(stream):
+    return stream if stream is None or isinstance(stream, int) else stream.cuda_stream
 
 
 def batq_linear_w4a16(X, A, B, w_codes, w_scales, M, out, w_gs=None, w_format=BATQ_W4_MXFP4, stream=None):
     """out = (X P) W'^T of 1 to 16 tokens with prepared 4-bit weights (A = B = None: no transform)."""
-    T, dev, st = _serving(stream)
-    N = X.shape[-1]
-    x, xt, S, ldx = _matrix(T, X, N, dev, "X")
-    o, ot, rows, ldo = _matrix(T, out, M, dev, "out")
-    if rows != S:
-        raise ValueError(f"out must have {S} rows, got {rows}")
-    a = a_keep = None
-    if A is not None:
-        a, a_keep = _factor(A, 64, "A")
-    _status(T.lib.batq_linear_w4a16(
-        x, xt, S, N, ldx, a, None if B is None else _array(B, T.f32, dev, "B", N // 32 * 16), w_format,
-        _array(w_codes, T.u8, dev, "w_codes", M * N // 2),
-        _array(w_scales, T.u8, dev, "w_scales", _mma_scale_bytes(M, N // (32 if w_format == BATQ_W4_MXFP4 else 16))),
-        None if w_gs is None else _array(w_gs, T.f32, dev, "w_gs", 1), M, ot, o, ldo, st), "batq_linear_w4a16")
+    f = (_SERVING or _load_serving()).linear_w4a16
+    status = f(X, A, B, w_codes, w_scales, M, out, w_gs, w_format, _raw(stream))
+    if status == _CONVERT:
+        status = f(X, _host_f32(A, 64, "A"), B, w_codes, w_scales, M, out, w_gs, w_format, _raw(stream))
+    if status:
+        raise BatqError(status, "batq_linear_w4a16")
 
 
 def batq_kv8_append(K, V, cu_new, seq_lens, page_table, k_codes, k_scales, v_codes, v_scales, stream=None):
     """New K and V rows (T x kv_heads * head_dim) into the 8-bit paged cache; cu_new None: one per sequence."""
-    T, dev, st = _serving(stream)
-    (kc, ks, vc, vs), P, H, page, D = _kv8_cache(T, k_codes, k_scales, v_codes, v_scales, dev)
-    k, kt, rows, ldk = _matrix(T, K, H * D, dev, "K")
-    v, vt, vrows, ldv = _matrix(T, V, H * D, dev, "V")
-    if kt != vt or rows != vrows:
-        raise ValueError("K and V must have the same shape and type")
-    cu, lens, table, B, max_pages = _batch(T, cu_new, seq_lens, page_table, rows, dev, "cu_new")
-    _status(T.lib.batq_kv8_append(k, v, kt, rows, H, D, ldk, ldv, cu, lens, table, B, max_pages, P, page, kc, ks, vc,
-                                  vs, st), "batq_kv8_append")
+    status = (_SERVING or _load_serving()).kv8_append(K, V, cu_new, seq_lens, page_table, k_codes, k_scales, v_codes,
+                                                      v_scales, _raw(stream))
+    if status:
+        raise BatqError(status, "batq_kv8_append")
 
 
 def batq_attn_kv8_workspace_size(max_q_len: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
@@ -675,22 +590,10 @@ def batq_attn_kv8_workspace_size(max_q_len: int, q_heads: int, kv_heads: int, he
 def batq_attn_kv8(Q, cu_q, seq_lens, page_table, k_codes, k_scales, v_codes, v_scales, softmax_scale, max_q_len,
                   workspace, out, lse=None, stream=None):
     """Attention of Q (T x q_heads * head_dim) over the 8-bit paged cache; cu_q None: one query per sequence."""
-    T, dev, st = _serving(stream)
-    (kc, ks, vc, vs), P, H, page, D = _kv8_cache(T, k_codes, k_scales, v_codes, v_scales, dev)
-    row = Q.shape[-1]
-    q, qt, rows, ldq = _matrix(T, Q, row, dev, "Q")
-    o, ot, orows, ldo = _matrix(T, out, row, dev, "out")
-    if orows != rows or row % D:
-        raise ValueError("Q and out must be T x q_heads * head_dim")
-    cu, lens, table, B, max_pages = _batch(T, cu_q, seq_lens, page_table, rows, dev, "cu_q")
-    ws, ws_bytes = _bytes(workspace, dev, "workspace")
-    l = None
-    if lse is not None:
-        if lse.shape != (rows, row // D):
-            raise ValueError("lse must be T x q_heads")
-        l = _array(lse, T.f32, dev, "lse")
-    _status(T.lib.batq_attn_kv8(q, qt, rows, ldq, row // D, H, D, cu, lens, table, B, max_pages, P, page, kc, ks, vc, vs,
-                                softmax_scale, max_q_len, ws, ws_bytes, ot, o, ldo, l, st), "batq_attn_kv8")
+    status = (_SERVING or _load_serving()).attn_kv8(Q, cu_q, seq_lens, page_table, k_codes, k_scales, v_codes, v_scales,
+                                                    softmax_scale, max_q_len, workspace, out, lse, _raw(stream))
+    if status:
+        raise BatqError(status, "batq_attn_kv8")
 
 
 def empty_kv8_cache(num_pages: int, kv_heads: int, page_size: int, head_dim: int, device="cuda"):
@@ -703,14 +606,10 @@ def empty_kv8_cache(num_pages: int, kv_heads: int, page_size: int, head_dim: int
 
 def batq_gemm_mxfp4_experts(a_codes, a_scales, w_codes, w_scales, expert_offsets, M, N, out, stream=None):
     """Rows [offsets[e], offsets[e + 1]) of a (LINEAR scales) times expert e's weights (E x M x N/2)."""
-    T, dev, st = _serving(stream)
-    E = expert_offsets.numel() - 1
-    o, ot, rows, ldo = _matrix(T, out, M, dev, "out")
-    _status(T.lib.batq_gemm_mxfp4_experts(
-        _array(a_codes, T.u8, dev, "a_codes", rows * N // 2), _array(a_scales, T.u8, dev, "a_scales", rows * (N // 32)),
-        _array(w_codes, T.u8, dev, "w_codes", E * M * N // 2),
-        _array(w_scales, T.u8, dev, "w_scales", E * _mma_scale_bytes(M, N // 32)),
-        _array(expert_offsets, T.i32, dev, "expert_offsets"), E, rows, M, N, ot, o, ldo, st), "batq_gemm_mxfp4_experts")
+    status = (_SERVING or _load_serving()).gemm_mxfp4_experts(a_codes, a_scales, w_codes, w_scales, expert_offsets, M, N,
+                                                              out, _raw(stream))
+    if status:
+        raise BatqError(status, "batq_gemm_mxfp4_experts")
 
 
 def batq_linear_experts_workspace_size(T: int, N: int) -> int:
@@ -721,21 +620,12 @@ def batq_linear_experts_workspace_size(T: int, N: int) -> int:
 
 def batq_linear_experts(X, A, B, ratios, w_codes, w_scales, expert_offsets, M, workspace, out, stream=None):
     """Quantiser and experts' products of the sorted rows X (T x N) on one stream."""
-    T, dev, st = _serving(stream)
-    N = X.shape[-1]
-    E = expert_offsets.numel() - 1
-    x, xt, rows, ldx = _matrix(T, X, N, dev, "X")
-    o, ot, orows, ldo = _matrix(T, out, M, dev, "out")
-    if orows != rows:
-        raise ValueError(f"out must have {rows} rows, got {orows}")
-    a, a_keep = _factor(A, 64, "A")
-    ws, ws_bytes = _bytes(workspace, dev, "workspace")
-    _status(T.lib.batq_linear_experts(
-        x, xt, rows, N, ldx, a, _array(B, T.f32, dev, "B", N // 32 * 16),
-        None if ratios is None else _array(ratios, T.f32, dev, "ratios", N // 32 * 2),
-        _array(w_codes, T.u8, dev, "w_codes", E * M * N // 2),
-        _array(w_scales, T.u8, dev, "w_scales", E * _mma_scale_bytes(M, N // 32)),
-        _array(expert_offsets, T.i32, dev, "expert_offsets"), E, M, ws, ws_bytes, ot, o, ldo, st), "batq_linear_experts")
+    f = (_SERVING or _load_serving()).linear_experts
+    status = f(X, A, B, ratios, w_codes, w_scales, expert_offsets, M, workspace, out, _raw(stream))
+    if status == _CONVERT:
+        status = f(X, _host_f32(A, 64, "A"), B, ratios, w_codes, w_scales, expert_offsets, M, workspace, out, _raw(stream))
+    if status:
+        raise BatqError(status, "batq_linear_experts")
 
 
 def batq_selftest_wait_timeout(limit_us: int, stream=None):

@@ -5,8 +5,10 @@ Usage: python -m mxfp4_w4a4_post_block_b200.build [--force] [-v]
 Every translation unit under csrc/ is compiled to an object under _build/ (in
 parallel) and linked into ``libbatq.so`` next to this file, with the CUDA
 runtime linked statically so the library loads on machines without a GPU
-driver (CUDA calls then fail with BATQ_ERR_CUDA).  Sources are only rebuilt
-when they or a header changed.
+driver (CUDA calls then fail with BATQ_ERR_CUDA).  binding/serving.cpp becomes
+``_serving.so``, the Python module that marshals the serving calls' arguments
+(it uses torch's headers; the library itself does not).  Sources are only
+rebuilt when they or a header changed.
 """
 
 from __future__ import annotations
@@ -24,6 +26,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libbatq.so")
+SERVING_SRC = os.path.join(PKG, "binding", "serving.cpp")
+SERVING = os.path.join(PKG, "_serving.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -68,8 +72,29 @@ def _compile(src, verbose):
     return obj
 
 
+def _build_serving(force):
+    """Compile the _serving module against torch's headers and libbatq.so."""
+    import sysconfig
+
+    import torch
+
+    if not force and not _stale(SERVING, [SERVING_SRC, os.path.join(ROOT, "include", "batq.h")]):
+        return
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(base, "include"),
+           "-I" + os.path.join(base, "include", "torch", "csrc", "api", "include"), "-I" + os.path.join(cuda, "include"),
+           SERVING_SRC, "-o", SERVING, "-L" + PKG, "-l:libbatq.so", "-Wl,-rpath,$ORIGIN", "-L" + os.path.join(base, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on serving.cpp:\n{r.stdout}\n{r.stderr}")
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile and link libbatq.so; returns its path."""
+    """Compile and link libbatq.so and the _serving module; returns the library's path."""
     os.makedirs(BUILD, exist_ok=True)
     if force:
         for o in glob.glob(os.path.join(BUILD, "*.o")):
@@ -82,6 +107,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    _build_serving(force)
     return LIB
 
 
