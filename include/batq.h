@@ -615,9 +615,10 @@ typedef enum { BATQ_W4_MXFP4 = 0, BATQ_W4_NVFP4 = 1 } batq_w4_format;
  * A_host, B_dev: as batq_quant_act, or both NULL.
  * w_codes, w_scales: M rows, MMA scale layout.  w_gs_dev: NVFP4 only, the
  *    device float that batq_prepare_weights_nvfp4 wrote, or NULL (1).
- * Accuracy: y is kept to 22 bits relative to its token's largest value (bf16 X
- * without a transform exactly), products are exact and summed in fp32.
- * Non-finite x make the token's outputs non-finite (NaN, or an infinity).
+ * Accuracy: y is rounded to 2^-13 (bf16 out) or 2^-22 (fp32 out) of the power
+ * of two at or below the largest of its 32 neighbours (NVFP4: 16, and to 2^-25
+ * or 2^-34 of the token's largest); products are exact and summed in fp32.
+ * A non-finite x makes all outputs of its token NaN.
  * Errors: BATQ_ERR_INVALID_ARG (also: only one of A_host and B_dev, w_gs_dev
  * with MXFP4), BATQ_ERR_SHAPE (S > 16, N % 64 != 0 or N > 131072, M % 16 != 0),
  * BATQ_ERR_ALIGNMENT, BATQ_ERR_ARCH, BATQ_ERR_CUDA.
@@ -692,10 +693,15 @@ BATQ_API batq_status batq_attn_kv8_workspace_size(int max_q_len, int q_heads, in
  * belong to no sequence are not written.  What lies in the cache behind a
  * sequence, or behind the tokens that a query sees, does not reach it, NaN
  * included.
- * Accuracy: queries are rounded to f16 after an exact normalisation (bf16
- * queries lose nothing down to 2^-28 of the row's largest), probabilities to
- * f16; scores, sums and outputs are fp32 until the last rounding.  The split
- * of the work depends only on the lengths, so results repeat bit for bit.
+ * Accuracy: scores, sums and outputs are fp32 until the last rounding.  Head
+ * dims 64 and 256, and 128 with max_pages * page_size up to 2048: queries are
+ * rounded to f16 after an exact normalisation (bf16 queries lose nothing down
+ * to 2^-28 of the row's largest), the products of probability and V scale to
+ * f16, and to 2^-40 of the row's largest.  Head dim 128 with longer tables:
+ * bf16 queries lose nothing down to 2^-13 of the largest of their 32 head dims,
+ * fp32 queries keep 12 bits, and those products are rounded to 2^-20 of the
+ * largest among their 32 tokens.  The split of the work depends only on the
+ * lengths, so results repeat bit for bit.  Non-finite queries give NaN.
  * workspace: device, 16-byte aligned; calls that may overlap need one each.
  * Errors: BATQ_ERR_INVALID_ARG (softmax_scale not finite), BATQ_ERR_SHAPE,
  * BATQ_ERR_ALIGNMENT, BATQ_ERR_WORKSPACE, BATQ_ERR_ARCH, BATQ_ERR_CUDA.

@@ -38,7 +38,8 @@ batq_status check_kv8(int T, int kv_heads, int head_dim, const int* cu_dev, cons
   if (head_dim != 64 && head_dim != 128 && head_dim != 256) return BATQ_ERR_SHAPE;
   if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128) return BATQ_ERR_SHAPE;
   if (kv_heads > 1024 || batch > 65535) return BATQ_ERR_SHAPE;
-  if ((long long)max_pages * page_size >= (1LL << 31)) return BATQ_ERR_SHAPE;
+  // Token numbers stay 32-bit for some tiles of a look ahead behind the longest sequence.
+  if ((long long)max_pages * page_size > (1LL << 31) - 16384) return BATQ_ERR_SHAPE;
   if ((long long)num_pages * kv_heads * page_size >= (1LL << 31)) return BATQ_ERR_SHAPE;  // cache rows
   if (!cu_dev && T < batch) return BATQ_ERR_SHAPE;
   if (!aligned(seq_lens_dev, 4) || !aligned(page_table_dev, 4) || (cu_dev && !aligned(cu_dev, 4)) ||

@@ -27,25 +27,27 @@
 // (m, l, o) partials in the workspace (at most two per CTA: its first and its last item), joined in
 // key order by k_attn_kv8_join.  Within a CTA, kKW key groups take every kKW-th tile, each with a
 // ring of its own (K and V tiles in turn), and kRW warps of a group share its tiles for further rows.
+//
+// What bounds it is the issue of instructions: widening K and V, the softmax's and the loads' address
+// arithmetic are about 820 of them per 32 keys and 8 rows, at half of the issue slots; so head dim 128 with
+// long page tables has the kernel in attn_kv8_tc.cu.  Measured: 16 sequences of up to 16000 tokens, 4 heads of
+// 8 queries: 31 us at head dim 64 (3.6 TB/s), 64 us at 256 (4.6 TB/s); 3 sequences of 100 tokens 6 us, the
+// launch and one tile's way through it.  More rows cost more softmax: five queries each 70 and 123 us.
 #include <cstdint>
 #include <type_traits>
 
-#include "host_util.h"
-#include "kernels.h"
-#include "kv8.cuh"
-#include "ptx.cuh"
+#include "attn_kv8.cuh"
 
 namespace batq {
 namespace {
 
 constexpr int kTile = 32;  // keys per tile
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 
 // kD: head dim; kNT: 8-row tiles per warp; kRW: row warps; kKW: key groups; kSlots: ring slots (a K or
 // a V tile each) per key group; kCtas: CTAs per SM that registers and shared memory are laid out for.
 template <int kD_, int kNT_, int kRW_, int kKW_, int kSlots_, int kCtas_>
 struct AttnCfg {
+  static constexpr int kOver = 0;
   static constexpr int kD = kD_, kNT = kNT_, kRW = kRW_, kKW = kKW_, kSlots = kSlots_, kCtas = kCtas_;
   static constexpr int kRowsPerWarp = 8 * kNT;
   static constexpr int kRows = kRowsPerWarp * kRW;
@@ -63,75 +65,6 @@ struct AttnCfg {
   static constexpr int kSmallBytes = kRows * 4 + 2 * kKW * kRows * 4 + 2 * kKW * kSlots * 8 + kKW * kMetas * 32 + 64;
   static constexpr int kSmemBytes = kDataBytes + kQBytes + kSmallBytes + 1024;
 };
-
-struct AttnArgs {
-  const void* Q;
-  int T, ldq, q_heads, kv_heads, group;
-  const int* cu_q;
-  const int* seq_lens;
-  const int* page_table;
-  int batch, max_pages, num_pages, page_size, page_shift;
-  const uint8_t* k_scales;
-  const uint8_t* v_scales;
-  float scale_log2;
-  int max_q_len;
-  int runs;            // CTAs of the main kernel
-  float* partial;      // [2 * runs][rows][D], then m and l: [2 * runs][rows] each
-  int out_bf16;
-  void* out;
-  int ldo;
-  float* lse;
-  unsigned* err;
-};
-
-// Work units of sequence b: kv_heads * row tiles * key blocks (none without queries).
-struct Items {
-  SeqRows s;       // count: the queries to compute
-  int queries;     // all of the sequence's, which places them
-  int row_tiles, key_blocks;
-  __device__ int units(int kv_heads) const { return kv_heads * row_tiles * key_blocks; }
-};
-template <class C>
-__device__ __forceinline__ Items items_of(const AttnArgs& a, int b) {
-  Items it;
-  it.s = seq_rows(a.cu_q, a.seq_lens, b, a.T, a.max_pages * a.page_size);
-  it.s.len = max(it.s.len, 0);
-  it.queries = it.s.count;
-  it.s.count = min(it.s.count, a.max_q_len);
-  it.row_tiles = (it.s.count * a.group + C::kRows - 1) / C::kRows;
-  it.key_blocks = max(1, (it.s.len + C::kUnit - 1) / C::kUnit);  // an empty sequence still writes its zeros
-  return it;
-}
-
-// The W units of the list in R runs of W / R, the first W % R of them one longer.
-struct Runs {
-  int count, size, longer;
-  __device__ int begin(int r) const { return r * size + min(r, longer); }
-  // Run of unit u.
-  __device__ int of(int u) const {
-    const int head = longer * (size + 1);
-    return u < head ? u / (size + 1) : longer + (u - head) / size;
-  }
-};
-__device__ __forceinline__ Runs runs_of(int W, int runs) {
-  Runs r;
-  r.count = min(W, runs);
-  r.size = W / max(r.count, 1);
-  r.longer = W - r.size * r.count;
-  return r;
-}
-
-// Units in all, and those before sequence b, by one warp (every lane gets them).
-template <class C>
-__device__ __forceinline__ int2 count_units(const AttnArgs& a, int b, int lane) {
-  int w = 0, before = 0;
-  for (int q = lane; q < a.batch; q += 32) {
-    const int n = items_of<C>(a, q).units(a.kv_heads);
-    w += n;
-    before += q < b ? n : 0;
-  }
-  return make_int2(__reduce_add_sync(0xffffffffu, w), __reduce_add_sync(0xffffffffu, before));
-}
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -151,12 +84,6 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi) {
       : "r"(w));
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %2, %1;" : "=r"(r) : "f"(lo), "f"(hi));
@@ -168,26 +95,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
-}
-
-// V's page scales ride on the scores: with x_t the score in log2 units and 2^ev(t) the scale of token
-// t's V block, the weights in the matrix instruction are p_t = 2^(x_t + ev(t) - m + kBias), m the
-// running maximum of x + ev, and the sum takes p_t 2^-(ev(t) + kBias) = 2^(x_t - m).  So f16 keeps 11
-// bits of every weight that matters beside the row's largest product of probability and scale (the
-// bias puts that one at 2^15, and f16's smallest step 2^39 below it) however far apart the blocks'
-// scales are, and the accumulators need no unit of their own.  Scales below 2^kMinExp (an all-zero
-// block has 2^-127) ride as 2^kMinExp, which keeps the sum inside fp32, and the rest multiplies the
-// f16 weights.
-constexpr int kBias = 15;
-constexpr int kMinExp = -100;
-constexpr float kUnbias = 1.0f / 32768.0f;
-__device__ __forceinline__ float v_exponent(int byte) {
-  return byte == 255 ? __uint_as_float(0x7FC00000u) : (float)max(byte - 127, kMinExp);
-}
-
-// Bit 7 of every byte that is an E4M3 NaN (all of its low seven bits set).
-__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
-  return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
 }
 
 __device__ __forceinline__ uint32_t lds32(const uint8_t* p) { return *reinterpret_cast<const uint32_t*>(p); }
@@ -402,6 +309,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
         for (int i = 0; i < kPer; ++i) {
           const float m = fabsf(v[i]);
           amax = m <= 3.402823466e38f ? fmaxf(amax, m) : amax;
+          v[i] = m <= 3.402823466e38f ? v[i] : __uint_as_float(0x7FC00000u);  // (infinite scores could sum to nothing)
         }
       } else {
 #pragma unroll
@@ -553,8 +461,10 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             p[e] = ex2(fmaf(s[mk][n][e], rf[n][e & 1] * hh.x, mk == 0 ? b0[e & 1] : b1[e & 1]));
-            if (!kWhole && ((masked >> (4 * mk + e)) & 1u)) p[e] = 0.0f;
-            l[n][e & 1] = fmaf(p[e], hh.z, l[n][e & 1]);
+            if (!kWhole && ((masked >> (4 * mk + e)) & 1u))
+              p[e] = 0.0f;  // (a NaN scale is not for this row's sum either)
+            else
+              l[n][e & 1] = fmaf(p[e], hh.z, l[n][e & 1]);
           }
           if (hh.y == (float)kMinExp) {
             const float f = e8m0_value((uint32_t)(((__float_as_int(h1.w) >> (8 * mk)) & 255) - kMinExp));
@@ -727,140 +637,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
   }
 }
 
-// Joins the partials of the items cut by run borders.  kJW warps per row take its partials in turn
-// (warp w every kJW-th, in key order), then their sums are added in order.
-constexpr int kJoinWarps = 8;
-template <class C, int kJW>
-__global__ void __launch_bounds__(32 * kJoinWarps) k_attn_kv8_join(const AttnArgs a, const int most_rows) {
-  constexpr int kD = C::kD, kRows = C::kRows, kPer = kD / 32, kRowsPerCta = kJoinWarps / kJW;
-  __shared__ float s_acc[kJoinWarps][kD];
-  __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
-  griddep_wait();
-  griddep_launch_dependents();
-  const int lane = threadIdx.x & 31, slot = threadIdx.x >> 5, warp = slot % kJW, first = slot - warp;
-  const int b = blockIdx.y, x = blockIdx.x * kRowsPerCta + slot / kJW;
-  const int h = x / most_rows, rr = x - h * most_rows;  // kv head, row of the (sequence, kv head)
-  const Items it = items_of<C>(a, b);
-  if (h >= a.kv_heads || rr >= it.s.count * a.group) return;  // (all warps of a row together)
-  const int rt = rr / kRows, r = rr - rt * kRows;
-  const int2 W = count_units<C>(a, b, lane);
-  const Runs runs = runs_of(W.x, a.runs);
-  const int u0 = W.y + (h * it.row_tiles + rt) * it.key_blocks;
-  const int r0 = runs.of(u0), r1 = runs.of(u0 + it.key_blocks - 1);
-  if (r0 == r1) return;  // written by its CTA
-  const int slot0 = 2 * r0 + (runs.begin(r0) == u0 ? 0 : 1);
-  const float* ml = a.partial + (size_t)2 * a.runs * kRows * kD;
-  const float* ll = ml + (size_t)2 * a.runs * kRows;
-  float mx = -INFINITY, sum = 0.0f, acc[kPer];
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) acc[i] = 0.0f;
-  constexpr int kFlight = kJW == 1 ? 4 : 8;  // partials in flight per warp
-  for (int c0 = r0 + warp; c0 <= r1; c0 += kFlight * kJW) {
-    float pm[kFlight], pl[kFlight], v[kFlight][kPer];
-#pragma unroll
-    for (int k = 0; k < kFlight; ++k) {
-      const int c = c0 + k * kJW;
-      pm[k] = -INFINITY;
-      pl[k] = 0.0f;
-      if (c <= r1) {
-        const size_t at = (size_t)(c == r0 ? slot0 : 2 * c) * kRows + r;
-        pm[k] = ml[at];
-        pl[k] = ll[at];
-#pragma unroll
-        for (int i = 0; i < kPer; i += 2) {
-          const float2 x = *reinterpret_cast<const float2*>(a.partial + at * kD + lane * kPer + i);
-          v[k][i] = x.x;
-          v[k][i + 1] = x.y;
-        }
-      }
-    }
-    float m_new = mx;
-#pragma unroll
-    for (int k = 0; k < kFlight; ++k) m_new = fmaxf(m_new, pm[k]);
-    // Without any maximum there is nothing to weigh (sums of zero, or of NaN).
-    const float alpha = m_new == -INFINITY ? 1.0f : exp2f(mx - m_new);
-    sum *= alpha;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) acc[i] *= alpha;
-#pragma unroll
-    for (int k = 0; k < kFlight; ++k) {
-      if (c0 + k * kJW > r1) break;
-      const float w = m_new == -INFINITY ? 1.0f : exp2f(pm[k] - m_new);
-      sum = fmaf(w, pl[k], sum);
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) acc[i] = fmaf(w, v[k][i], acc[i]);
-    }
-    mx = m_new;
-  }
-  const size_t row = (size_t)(it.s.begin + rr / a.group);
-  const int head = h * a.group + rr % a.group;
-  const size_t o = row * (size_t)a.ldo + (size_t)head * kD;
-  if constexpr (kJW > 1) {
-    if (lane == 0) {
-      s_m[slot] = mx;
-      s_l[slot] = sum;
-    }
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) s_acc[slot][lane * kPer + i] = acc[i];
-    asm volatile("bar.sync %0, %1;" ::"r"(1 + first / kJW), "n"(32 * kJW) : "memory");
-    if (warp != 0) return;
-    mx = s_m[first];
-#pragma unroll
-    for (int w = 1; w < kJW; ++w) mx = fmaxf(mx, s_m[first + w]);
-    sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) acc[i] = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kJW; ++w) {
-      const float weight = mx == -INFINITY ? 1.0f : exp2f(s_m[first + w] - mx);
-      sum = fmaf(weight, s_l[first + w], sum);
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) acc[i] = fmaf(weight, s_acc[first + w][lane * kPer + i], acc[i]);
-    }
-  }
-  const float inv = sum == 0.0f ? 0.0f : kUnbias / sum;  // a row that sees nothing: zeros
-#pragma unroll
-  for (int i = 0; i < kPer; i += 2) {
-    if (a.out_bf16)
-      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + o + lane * kPer + i) =
-          pack_bf16x2(acc[i] * inv, acc[i + 1] * inv);
-    else
-      *reinterpret_cast<float2*>(static_cast<float*>(a.out) + o + lane * kPer + i) =
-          make_float2(acc[i] * inv, acc[i + 1] * inv);
-  }
-  if (a.lse && lane == 0) a.lse[row * a.q_heads + head] = sum == 0.0f ? -INFINITY : kLn2 * (mx + log2f(sum));
-}
-
-constexpr int kMaxRuns = 592;  // 148 SMs x 4 CTAs
-
 template <class C>
 cudaError_t launch_cfg(const AttnKv8Launch& L, cudaStream_t stream) {
-  AttnArgs a = {};
-  a.Q = L.Q;
-  a.T = L.T;
-  a.ldq = L.ldq;
-  a.q_heads = L.q_heads;
-  a.kv_heads = L.kv_heads;
-  a.group = L.q_heads / L.kv_heads;
-  a.cu_q = L.cu_q;
-  a.seq_lens = L.seq_lens;
-  a.page_table = L.page_table;
-  a.batch = L.batch;
-  a.max_pages = L.max_pages;
-  a.num_pages = L.num_pages;
-  a.page_size = L.page_size;
-  a.page_shift = L.page_size == 16 ? 4 : L.page_size == 32 ? 5 : L.page_size == 64 ? 6 : 7;
-  a.k_scales = L.k_scales;
-  a.v_scales = L.v_scales;
-  a.scale_log2 = L.softmax_scale * kLog2e;
-  a.max_q_len = L.max_q_len;
-  a.partial = L.workspace;
-  a.out_bf16 = L.out_bf16 ? 1 : 0;
-  a.out = L.out;
-  a.ldo = L.ldo;
-  a.lse = L.lse;
-  a.err = L.err;
-
   auto kern = k_attn_kv8<C>;
   static int occ[64] = {0};
   int dev = 0;
@@ -874,7 +652,7 @@ cudaError_t launch_cfg(const AttnKv8Launch& L, cudaStream_t stream) {
     occ[dev] = n < 1 ? 1 : n;
   }
   const int slots = sm_count() * occ[dev];
-  a.runs = slots < kMaxRuns ? slots : kMaxRuns;
+  const AttnArgs a = attn_args(L, slots < kMaxRuns ? slots : kMaxRuns);
 
   CUtensorMap tm_k, tm_v;
   const uint64_t rows = (uint64_t)L.num_pages * L.kv_heads * L.page_size;
@@ -896,17 +674,7 @@ cudaError_t launch_cfg(const AttnKv8Launch& L, cudaStream_t stream) {
   cfg.numAttrs = 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tm_k, tm_v, a, L.q_bf16 ? 1 : 0);
   if (e != cudaSuccess) return e;
-  // No sequence can be longer than its page table: when that is one unit, no item is ever cut.
-  if ((long long)L.max_pages * L.page_size <= C::kUnit) return cudaSuccess;
-  const long long rows_most = (long long)L.max_q_len * a.group, rows_all = rows_most * L.kv_heads;
-  if (rows_all >= (1LL << 31) - 8) return cudaErrorInvalidConfiguration;
-  // With at least a quarter as many items as runs an item has about four partials at most: a warp per row.
-  const bool few = (long long)L.batch * L.kv_heads * 4 >= a.runs;
-  cfg.gridDim = dim3((unsigned)(few ? (rows_all + kJoinWarps - 1) / kJoinWarps : rows_all), (unsigned)L.batch);
-  cfg.blockDim = dim3(32 * kJoinWarps);
-  cfg.dynamicSmemBytes = 0;
-  return few ? cudaLaunchKernelEx(&cfg, k_attn_kv8_join<C, 1>, a, (int)rows_most)
-             : cudaLaunchKernelEx(&cfg, k_attn_kv8_join<C, kJoinWarps>, a, (int)rows_most);
+  return launch_join<C>(L, a, stream);
 }
 
 // Rows of an item by the most rows a sequence can have (queries times heads per kv head).
@@ -919,7 +687,7 @@ cudaError_t launch_rows(const AttnKv8Launch& L, cudaStream_t stream) {
   if (rows <= 8) return launch_cfg<AttnCfg<kD, 1, 1, 4, kSlots, kD == 256 ? 2 : 4>>(L, stream);
   if (rows <= 16) return launch_cfg<AttnCfg<kD, 2, 1, 4, kSlots, kD == 256 ? 1 : 3>>(L, stream);
   if (rows <= 32 || kD == 256) return launch_cfg<AttnCfg<kD, 2, 2, 2, 4, kD == 256 ? 1 : 3>>(L, stream);
-  return launch_cfg<AttnCfg<kD == 256 ? 128 : kD, 3, 2, 2, 4, 3>>(L, stream);
+  return launch_cfg<AttnCfg<kD == 256 ? 128 : kD, 3, 2, 2, 4, kD == 64 ? 3 : 2>>(L, stream);
 }
 
 int rows_per_item(long long rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 48; }
@@ -934,7 +702,13 @@ size_t attn_kv8_workspace_bytes(int max_q_len, int q_heads, int kv_heads, int he
 cudaError_t launch_attn_kv8(const AttnKv8Launch& L, cudaStream_t stream) {
   switch (L.head_dim) {
     case 64: return launch_rows<64>(L, stream);
-    case 128: return launch_rows<128>(L, stream);
+    case 128:
+      // The other kernel's items cost more beside their keys, so it takes the calls whose page tables allow long
+      // sequences (the lengths are not known here).  Measured, this kernel and that: 128 sequences of up to 2000
+      // tokens 62 and 70 us, of up to 500 40 and 44 us, 64 of up to 400 with 40 rows 35 and 50 us; 64 of up to
+      // 8192 125 and 103 us, 16 of up to 4000 with 320 rows 167 and 96 us.
+      if ((long long)L.max_pages * L.page_size > 2048) return launch_attn_kv8_tc(L, stream);
+      return launch_rows<128>(L, stream);
     case 256: return launch_rows<256>(L, stream);
   }
   return cudaErrorInvalidValue;

@@ -105,10 +105,11 @@ def append(x, cu, lens, table, page, vals, exps):
                 vals[pid, h, o:o + hi - lo] = q
 
 
-def attention(q, cu, lens, table, page, k, v, vs, scale, max_q, q_bits=24):
+def attention(q, cu, lens, table, page, k, v, vs, scale, max_q, q_bits=24, digits=False):
     """q: T x H x D fp64; k, v: [pages, heads, page, D] fp64 values; vs: [pages, heads] the scales in v.  Returns (out, lse, tol): rows without a
     sequence are NaN in tol.  tol: what f16 probabilities (2^-11 each, weights and none in the sum), scores
-    off by their fp32 sums and by queries of `q_bits` bits, and fp32 sums of p v may move an output by."""
+    off by their fp32 sums and by queries of `q_bits` bits, and fp32 sums of p v may move an output by.  `digits`:
+    of weights that are integers of 20 bits per 32 tokens instead, and of queries in 8-bit parts."""
     T, H, D = q.shape
     heads = k.shape[1]
     G = H // heads
@@ -147,6 +148,22 @@ def attention(q, cu, lens, table, page, k, v, vs, scale, max_q, q_bits=24):
                 # ds << 1, and scores of 1e5 have ds > 1).
                 ds = c.max() * (2.0 ** -q_bits + (D / 8 + 8) * 2.0 ** -23) + np.abs(s).max() * 2.0 ** -22 + 2.0 ** -15
                 pv = (p / l) @ np.abs(vals)
+                if digits:
+                    # A query's parts: E4M3 keeps a value to 2^-4 of it or to 2^-10, where the largest of 32 head dims
+                    # is in [2^7, 2^8), and each further part divides that by 16.  Two parts hold bf16's bits but for
+                    # the second bound, 2^-14 / 2^7; three keep fp32 to 2^-12 of the value or 2^-18 / 2^7.
+                    top = np.repeat(np.abs(qq).reshape(-1, 32).max(1), 32)
+                    eq = top * 2.0 ** -21 if q_bits > 11 else np.abs(qq) * 2.0 ** -12 + top * 2.0 ** -25
+                    ds = (np.abs(ks) @ eq).max() * abs(scale) + c.max() * (D / 8 + 8) * 2.0 ** -23 + np.abs(s).max() * 2.0 ** -22 + 2.0 ** -15
+                    grow = np.expm1(min(2 * ds, 600.0))
+                    # The integers are off by half a unit, 2^-21 of a power of two that is less than twice the largest
+                    # weight of the 32 tokens; the exponential by 2^-21; each tile's additions round in fp32.
+                    at = np.nonzero(see)[0] // 32
+                    most = np.zeros(at.max() + 1)
+                    np.maximum.at(most, at, p * sc)
+                    tol[r0 + i, h] = pv * (2.0 ** -20 + (L / 32 + 8) * 2.0 ** -23 + grow)
+                    tol[r0 + i, h] += 2.0 ** -20 / l * (1 + grow) * (most[at] @ np.abs(vals / sc[:, None]))
+                    continue
                 tol[r0 + i, h] = pv * (2.0 ** -11 + 2.0 ** -20 + np.expm1(min(2 * ds, 600.0)) * (1 + 2.0 ** -11))
                 # The f16 weights are p_t 2^ev(t) over the largest such product W, times 2^15: below 2^-14 their
                 # rounding is absolute, 2^-25, that is 2^-40 W for each token's code.

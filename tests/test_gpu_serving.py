@@ -263,7 +263,8 @@ def attn_check(out, lse, q, cu, lens, table, kc, ks, vc, vs, scale, max_q):
     k = R.e4m3_value(kc) * R.e8m0_value(ks)[..., None, None]
     v = R.e4m3_value(vc) * R.e8m0_value(vs)[..., None, None]
     qd = q.double().numpy().reshape(T, -1, D)
-    ref, rlse, tol = R.attention(qd, cu, lens, table, page, k, v, R.e8m0_value(vs), scale, max_q, 23 if q.dtype == BF else 11)
+    ref, rlse, tol = R.attention(qd, cu, lens, table, page, k, v, R.e8m0_value(vs), scale, max_q, 23 if q.dtype == BF else 11,
+                             digits=D == 128 and table.shape[1] * page > 2048)
     got, mine = host(out).reshape(ref.shape), ~np.isnan(tol).all(2)
     assert (got[~mine] == 7).all(), "rows of no sequence were written"
     tol = tol + np.abs(ref) * (2.0 ** -8 if out.dtype == BF else 2.0 ** -22) + 2.0 ** -140
@@ -428,6 +429,196 @@ def test_attention_nan_does_not_pass_the_mask(page, D):
     vc2[0, 0, 3, 7] = 0x7F  # in a tile that every query sees whole
     out, _ = attn_run(q, cu, lens, table, kc, ks, vc2, vs, 0.1, n)
     assert out.view(n, G, D)[:, :, 7].isnan().all() and torch.equal(out.view(n, G, D)[:2, :, 8:], clean.view(n, G, D)[:2, :, 8:])
+
+
+def long_table(c, page, tokens=2049):
+    """The same call with a page table for more than 2048 tokens, which head dim 128 has a kernel of its own for."""
+    c = list(c)
+    more = -(-tokens // page) - c[3].shape[1]
+    c[3] = np.concatenate([c[3], np.full((c[3].shape[0], max(more, 0)), -1, np.int32)], 1)
+    return c
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("B,kv,G,most,q_most", [(1, 1, 1, 5, 1), (3, 2, 1, 300, 1), (5, 2, 4, 700, 2), (4, 1, 7, 500, 3),
+                                               (2, 3, 8, 900, 8), (3, 1, 16, 400, 2), (7, 2, 5, 40, 6), (9, 1, 9, 1500, 1),
+                                               (2, 2, 6, 800, 5), (2, 1, 48, 700, 3)])
+def test_long_attention_ragged(B, kv, G, most, q_most, page):
+    c = long_table(attn_case(B * 100 + G + page, B, kv, G, 128, page, most, q_most, pad=2), page)
+    out, lse = attn_run(*c, 128 ** -0.5, q_most)
+    attn_check(out, lse, *c, 128 ** -0.5, q_most)
+
+
+@pytest.mark.parametrize("G,q_most", [(4, 1), (4, 3), (4, 8), (8, 6)])
+@pytest.mark.parametrize("q_dtype,out_dtype", [(F32, F32), (BF, F32), (F32, BF)])
+def test_long_attention_types(q_dtype, out_dtype, G, q_most):
+    c = long_table(attn_case(7, 4, 2, G, 128, 16, 500, q_most, q_dtype=q_dtype), 16)
+    out, lse = attn_run(*c, -0.09 if G == 8 else 0.09, q_most, out_dtype=out_dtype)
+    attn_check(out, lse, *c, -0.09 if G == 8 else 0.09, q_most)
+
+
+@pytest.mark.parametrize("G,q_most", [(4, 1), (3, 9), (8, 40)])
+def test_long_attention_is_split_and_joined(G, q_most):
+    """Many key blocks of few items, so that the runs' borders cut them; row tiles beyond one; bit for bit twice."""
+    rng = np.random.default_rng(9)
+    kv, D, page = 1, 128, 64
+    lens = np.array([30011, 9000, 0], np.int32)
+    cu = np.array([0, q_most, q_most + 1, q_most + 2], np.int32)
+    need = (lens + page - 1) // page
+    ids = rng.permutation(int(need.sum())).astype(np.int32)
+    table = np.full((3, need.max()), -1, np.int32)
+    table[0, :need[0]], table[1, :need[1]] = ids[:need[0]], ids[need[0]:]
+    kc, ks = R.cache(rng, len(ids), kv, page, D)
+    vc, vs = R.cache(rng, len(ids), kv, page, D)
+    q = torch.from_numpy(rng.standard_normal((int(cu[-1]), G * D)).astype(np.float32)).to(BF)
+    c = (q, cu, lens, table, kc, ks, vc, vs)
+    out, lse = attn_run(*c, 0.088, q_most)
+    attn_check(out, lse, *c, 0.088, q_most)
+    again, lse2 = attn_run(*c, 0.088, q_most)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("G", [4, 20])
+@pytest.mark.parametrize("spread", [0.0, 4.0, 12.0])
+def test_long_attention_page_scales_far_apart(spread, G):
+    """K and V pages whose scales differ by many powers of two: references move, digits lose the small blocks."""
+    c = long_table(attn_case(10, 3, 2, G, 128, 16, 400, 1, spread=spread), 16)
+    out, lse = attn_run(*c, 0.01, 1)
+    attn_check(out, lse, *c, 0.01, 1)
+
+
+@pytest.mark.parametrize("low,high", [(0, 5), (0, 247), (27, 120), (20, 130)])
+def test_long_attention_smallest_and_largest_page_scales(low, high):
+    c = long_table(attn_case(20, 4, 1, 2, 128, 16, 200, 1, spread=0.0), 16)
+    rng = np.random.default_rng(20)
+    c[7] = np.where(rng.random(c[7].shape) < 0.5, low, high).astype(np.uint8)
+    if low == 0 and high > 100:
+        c[6][c[7][:, 0] == 0] = 0
+    table, lens = c[3], c[2]
+    for b in range(2):  # two sequences of low pages only
+        c[7][table[b, :(lens[b] + 15) // 16]] = low
+    out, lse = attn_run(*c, 0.05, 1, out_dtype=F32)
+    attn_check(out, lse, *c, 0.05, 1)
+
+
+@pytest.mark.parametrize("scale", [0.125, 0.0])
+def test_long_attention_sharp_and_extreme_queries(scale):
+    """Scores of hundreds that grow along the sequence, zero, tiny and huge queries (their rows share an item)."""
+    c = long_table(attn_case(11, 5, 1, 4, 128, 32, 300, 1, spread=0.0), 32)
+    c[0][0] *= 40.0
+    c[0][1] = 0.0
+    c[0][2, :128] *= 1e30 if scale == 0.0 else 1.0
+    c[0][2, 128:256] *= 1e-30
+    c[5] = np.minimum(c[5], 30).astype(np.uint8) if scale == 0.0 else c[5]
+    ids = c[3][4, :(c[2][4] + 31) // 32]
+    c[5][ids] = (c[5][ids].astype(np.int64) + np.arange(len(ids))[:, None] // 2).astype(np.uint8)
+    out, lse = attn_run(*c, scale, 1)
+    attn_check(out, lse, *c, scale, 1)
+
+
+def test_long_attention_masks_leave_rows_empty():
+    rng = np.random.default_rng(12)
+    page, kv, G, D = 16, 2, 2, 128
+    kc, ks = R.cache(rng, 8, kv, page, D)
+    vc, vs = R.cache(rng, 8, kv, page, D)
+    table = np.array([[0, 1, 2], [3, 4, 5], [-1, 6, 99], [7, 0, 1], [2, 3, 4]], np.int32)
+    lens = np.array([0, 2, 40, 70, 33], np.int32)
+    cu = np.array([0, 2, 6, 7, 9, 13], np.int32)
+    q = torch.from_numpy(rng.standard_normal((15, kv * G * D)).astype(np.float32)).to(BF)
+    for max_q in (4, 3):
+        c = long_table((q, cu, lens, table, kc, ks, vc, vs), page)
+        out, lse = attn_run(*c, 0.125, max_q)
+        attn_check(out, lse, *c, 0.125, max_q)
+
+
+@pytest.mark.parametrize("G", [2, 12])
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("D,tokens", [(64, 0), (128, 0), (128, 2049)])
+def test_attention_nan_scales_do_not_pass_the_mask(D, tokens, page, G):
+    """A NaN scale of K or V reaches the queries that see a token of its page, and no others."""
+    rng = np.random.default_rng(17)
+    kv, n = 1, 4
+    L = 3 * page + 2  # the last page holds two tokens: queries 0 and 1 see none of them
+    kc, ks = R.cache(rng, 5, kv, page, D)
+    vc, vs = R.cache(rng, 5, kv, page, D)
+    table = np.arange(5, dtype=np.int32)[None]
+    cu, lens = np.array([0, n], np.int32), np.array([L], np.int32)
+    q = torch.from_numpy(rng.standard_normal((n, kv * G * D)).astype(np.float32)).to(BF)
+    c = long_table((q, cu, lens, table, kc, ks, vc, vs), page, tokens)
+    clean, _ = attn_run(*c, 0.1, n)
+    for which in (5, 7):
+        for bad in (3, 4):  # page 4 lies behind the sequence
+            d = list(c)
+            d[which] = d[which].copy()
+            d[which][bad] = 255
+            out, _ = attn_run(*d, 0.1, n)
+            assert torch.equal(out[:2], clean[:2])
+            assert out[2:].isnan().all() if bad == 3 else torch.equal(out, clean)
+
+
+@pytest.mark.parametrize("D,tokens,G", [(64, 0, 2), (128, 0, 2), (256, 0, 9), (128, 2049, 2), (128, 2049, 9)])
+def test_attention_queries_that_are_not_finite(D, tokens, G):
+    """An infinity or NaN in a query makes that query's head NaN, whatever the signs of the keys, and no other."""
+    rng = np.random.default_rng(18)
+    page, kv, n, L = 32, 2, 3, 200
+    kc, ks = R.cache(rng, 7, kv, page, D)
+    vc, vs = R.cache(rng, 7, kv, page, D)
+    kc[..., 3] &= 0x7F  # keys of one sign: infinite scores of one sign
+    kc[..., 3] |= 1
+    cu, lens = np.array([0, n], np.int32), np.array([L], np.int32)
+    q = torch.from_numpy(rng.standard_normal((n, kv * G * D)).astype(np.float32)).to(BF)
+    c = long_table((q, cu, lens, np.arange(7, dtype=np.int32)[None], kc, ks, vc, vs), page, tokens)
+    clean, _ = attn_run(*c, 0.1, n)
+    for value in (float("-inf"), float("inf"), float("nan")):
+        c[0] = q.clone()
+        c[0].view(n, kv * G, D)[1, 1, 3] = value
+        out, lse = attn_run(*c, 0.1, n)
+        o = out.view(n, kv * G, D)
+        assert o[1, 1].isnan().all() and lse[1, 1].isnan()
+        o[1, 1] = clean.view(n, kv * G, D)[1, 1]
+        assert torch.equal(out, clean)
+
+
+@pytest.mark.parametrize("D,G", [(64, 2), (128, 2), (256, 9)])
+def test_attention_scale_zero_weighs_all_tokens_alike(D, G):
+    c = attn_case(19, 3, 2, G, D, 16, 100, 3)
+    out, lse = attn_run(*c, 0.0, 3)
+    attn_check(out, lse, *c, 0.0, 3)
+
+
+@pytest.mark.parametrize("G", [4, 12])
+@pytest.mark.parametrize("page", [16, 64])
+def test_long_attention_nan_does_not_pass_the_mask(page, G):
+    rng = np.random.default_rng(13)
+    kv, L, n, D, pages = 1, 139, 4, 128, 12
+    kc, ks = R.cache(rng, pages, kv, page, D)
+    vc, vs = R.cache(rng, pages, kv, page, D)
+    table = np.arange(pages, dtype=np.int32)[None]
+    cu, lens = np.array([0, n], np.int32), np.array([L], np.int32)
+    q = torch.from_numpy(rng.standard_normal((n, kv * G * D)).astype(np.float32)).to(BF)
+
+    def run(k, v):
+        return attn_run(*long_table((q, cu, lens, table, k, ks, v, vs), page), 0.1, n)[0].view(n, G, D)
+
+    clean = run(kc, vc)
+    kc2, vc2 = kc.copy(), vc.copy()
+    for t in range(L, pages * page):
+        kc2[t // page, 0, t % page] = 0x7F
+        vc2[t // page, 0, t % page] = 0xFF
+    assert torch.equal(run(kc2, vc2), clean)
+    t = L - 2  # seen by the last two queries
+    for d in (5, 40, D - 1):
+        vc2[t // page, 0, t % page, d] = 0x7F if d == 5 else 0xFF
+    o = run(kc2, vc2)
+    rest = [d for d in range(D) if d not in (5, 40, D - 1)]
+    assert o[2:, :, [5, 40, D - 1]].isnan().all()
+    assert torch.equal(o[:2], clean[:2]) and torch.equal(o[2:][..., rest], clean[2:][..., rest])
+    kc2[t // page, 0, t % page, 9] = 0x7F
+    o = run(kc2, vc2)
+    assert o[2:].isnan().all() and torch.equal(o[:2], clean[:2])
+    vc2[0, 0, 3, 7] = 0x7F  # in a tile that every query sees whole
+    o = run(kc, vc2)
+    assert o[:, :, 7].isnan().all() and torch.equal(o[:2, :, 8:], clean[:2, :, 8:])
 
 
 def test_attention_strided_queries_and_outputs():
