@@ -140,6 +140,19 @@ __device__ __forceinline__ void for_digits(F&& f) {
   for_digits_impl<kCount>(f, std::make_integer_sequence<int, kCount>{});
 }
 
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c;\n\t"
+      "mov.b64 a, {%2, %3};\n\t"
+      "mov.b64 b, {%4, %5};\n\t"
+      "mov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 a, a, b, c;\n\t"
+      "mov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
 // kN consecutive fp32 columns of this thread's TMEM lane.
 template <int kN>
 __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[kN]) {
@@ -247,89 +260,112 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the GEMMs with wide tiles, costs a commit and a barrier per stage: 9.8 instead of 8.4 us for one
     // tile of K = 4096.)  The loop runs warp-wide (warp-uniform state) with one elected lane issuing.
     const bool issuer = elect_one();
-    const int per_stage = 32 * a.S;  // items of a stage
+    if (issuer) {
+    const int whole_stages = a.N / kStageK;
+    // What the loop would work out for every stage: it is the issuing thread's own instructions that limit it.
+    const uint64_t dw0 = sdesc_kmajor_sw128(smem_u32(s_w)), dx0 = sdesc_kmajor_sw128(smem_u32(s_x));
+    const uint64_t dsw0 = sdesc_sf_atom(smem_u32(s_sw)), dsx0 = sdesc_sf_atom(smem_u32(s_sx));
+    const uint32_t t_sw0 = tmem + a.t_sw, t_sx0 = tmem + a.t_sx;
+    const uint32_t idesc = kNv ? idesc_nvf4(kRows, a.n) : idesc_mxf4(a.n, 0, 0);
+    [[maybe_unused]] const uint32_t idesc_odd = idesc_mxf4(a.n, 2, 2);
     int s = 0, it = 0, passes = 0;   // passes: digits known to be made
     uint32_t ph = 0;
     bool ok = true;
     for (int tile = cluster; tile < a.tiles && ok; tile += clusters, ++it) {
       const int buf = it & 1;
-      if (!mbar_wait_warp(&acc_empty[buf], ((it >> 1) & 1) ^ 1)) {
-        if (issuer) set_error(a.err, kErrDrainTimeout);
+      if (!mbar_wait(&acc_empty[buf], ((it >> 1) & 1) ^ 1)) {
+        set_error(a.err, kErrDrainTimeout);
         break;
       }
       tc_fence_after_sync();
       const uint32_t t_acc = tmem + buf * a.acc_stride;
       for (int st = st0; st < st1; ++st) {
         if (it == 0) {  // the stage's digits and their scales
-          const int need = (min((st - st0 + 1) * per_stage, a.S * ((k1 - k0) >> 3)) + kMakers - 1) / kMakers;
-          for (; passes < need && ok; ++passes) ok = mbar_wait_warp(&made[passes], 0);
+          const int need = ((st - st0 + 1) * a.S + kMakerWarps - 1) / kMakerWarps;
+          for (; passes < need && ok; ++passes) ok = mbar_wait(&made[passes], 0);
         }
-        if (!ok || !mbar_wait_warp(&full[s], ph)) {
-          if (issuer) set_error(a.err, kErrDataTimeout);
+        if (!ok || !mbar_wait(&full[s], ph)) {
+          set_error(a.err, kErrDataTimeout);
           ok = false;
           break;
         }
         tc_fence_after_sync();
-        if (issuer) {
-          const int nmma = min(4, (a.N - st * kStageK) >> 6);
-          const int atoms = kNv ? nmma : (nmma + 1) >> 1;
-          const uint32_t tsw = tmem + a.t_sw + s * (4 * kAtoms);
-          const uint32_t tsx = tmem + a.t_sx + (st - st0) * (4 * kAtoms);
-          const uint64_t dsw = sdesc_sf_atom(smem_u32(s_sw + s * kSfBytes));
-          const uint64_t dsx = sdesc_sf_atom(smem_u32(s_sx + (st - st0) * kSfBytes));
-          for (int i = 0; i < atoms; ++i) {
-            tc_cp_32x128b_warpx4(tsw + 4 * i, dsw + (uint64_t)(i * (kSfAtom >> 4)));
-            if (it == 0) tc_cp_32x128b_warpx4(tsx + 4 * i, dsx + (uint64_t)(i * (kSfAtom >> 4)));
-          }
-          const uint64_t dw = sdesc_kmajor_sw128(smem_u32(s_w + s * kStageBytes));
-          const uint64_t dx = sdesc_kmajor_sw128(smem_u32(s_x + (size_t)(st - st0) * (a.n * 128)));
-          for (int j = 0; j < nmma; ++j) {
-            const uint32_t acc = (st > st0 || j > 0) ? 1u : 0u;
+        {
+          const uint32_t tsw = t_sw0 + s * (4 * kAtoms), tsx = t_sx0 + (st - st0) * (4 * kAtoms);
+          const uint64_t dsw = dsw0 + (uint64_t)(uint32_t)(s * (kSfBytes >> 4));
+          const uint64_t dsx = dsx0 + (uint64_t)(uint32_t)((st - st0) * (kSfBytes >> 4));
+          const uint64_t dw = dw0 + (uint64_t)(uint32_t)(s * (kStageBytes >> 4));
+          const uint64_t dx = dx0 + (uint64_t)(uint32_t)((st - st0) * (a.n * 8));
+          auto copy = [&](int i) { tc_cp_32x128b_warpx4(tsw + 4 * i, dsw + (uint64_t)(i * (kSfAtom >> 4))); };
+          auto copy_x = [&](int i) { tc_cp_32x128b_warpx4(tsx + 4 * i, dsx + (uint64_t)(i * (kSfAtom >> 4))); };
+          auto mma = [&](int j, uint32_t acc) {
             if constexpr (kNv)
-              tc_mma_nvf4(t_acc, dw + (uint64_t)(j * 2), dx + (uint64_t)(j * 2), idesc_nvf4(kRows, a.n), tsw + 4 * j,
-                          tsx + 4 * j, acc);
+              tc_mma_nvf4(t_acc, dw + (uint64_t)(j * 2), dx + (uint64_t)(j * 2), idesc, tsw + 4 * j, tsx + 4 * j, acc);
             else
-              tc_mma_mxf4(t_acc, dw + (uint64_t)(j * 2), dx + (uint64_t)(j * 2),
-                          idesc_mxf4(a.n, (2 * j) & 3, (2 * j) & 3), tsw + 4 * (j >> 1), tsx + 4 * (j >> 1), acc);
+              tc_mma_mxf4(t_acc, dw + (uint64_t)(j * 2), dx + (uint64_t)(j * 2), (j & 1) ? idesc_odd : idesc,
+                          tsw + 4 * (j >> 1), tsx + 4 * (j >> 1), acc);
+          };
+          const uint32_t later = st > st0 ? 1u : 0u;
+          if (st < whole_stages) {
+            if (it == 0) {
+#pragma unroll
+              for (int i = 0; i < kAtoms; ++i) copy_x(i);
+            }
+#pragma unroll
+            for (int i = 0; i < kAtoms; ++i) copy(i);
+            mma(0, later);
+#pragma unroll
+            for (int j = 1; j < 4; ++j) mma(j, 1u);
+          } else {
+            const int nmma = (a.N - st * kStageK) >> 6, atoms = kNv ? nmma : (nmma + 1) >> 1;
+            for (int i = 0; i < atoms; ++i) {
+              copy(i);
+              if (it == 0) copy_x(i);
+            }
+            for (int j = 0; j < nmma; ++j) mma(j, j > 0 ? 1u : later);
           }
           tc_commit(&empty[s]);
           if (st == st1 - 1) tc_commit(&acc_full[buf]);
         }
-        __syncwarp();
         if (++s == a.ring) {
           s = 0;
           ph ^= 1;
         }
       }
     }
+    }
   } else {
     // ------------------------------ digits ------------------------------
     // A thread makes row b (eight values) of one 4 x 8 block of one token: u = column b of B^T against
-    // the block's four rows, y = u A (A from the parameter bank).
-    const int id = tid;
+    // the block's four rows, y = u A (A from the parameter bank).  A warp makes 32 rows (8 blocks, a stage)
+    // of one token at a time: unit q of the units in the order of the stages, within a stage token after
+    // token.  The instructions of that bound the start of a call (a unit of eight digits took 600, and 16
+    // warps share four schedulers), so all that is the warp's or the digit's is worked out once for it.
+    const int units = (st1 - st0) * a.S;
+    const uint32_t per_token = (65536u + (uint32_t)a.S - 1) / (uint32_t)a.S;  // q / S = q * this >> 16 (q < 4096)
+    auto stage_of = [&](int q) { return (int)(((uint32_t)q * per_token) >> 16); };
     const int rows = ((k1 - k0) >> 5) * 4;  // of each token
     if constexpr (kNv) {
       // E4M3 scales span 17 powers of two, so a token's blocks are scaled relative to a bound of its
       // largest magnitude: |y| <= max |x| |B|_1 |A|_1 over its blocks.
-      // A warp takes 32 rows of one token at a time, four such pieces in flight.
-      const int pieces = (rows + 31) >> 5;
-      for (int p0 = warp; p0 < a.S * pieces; p0 += 4 * kMakerWarps) {
+      // Four units in flight.
+      for (int q0 = warp; q0 < units; q0 += 4 * kMakerWarps) {
         float v[4][8];
         float4 br[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int p = p0 + j * kMakerWarps, s = p / pieces, x = (p - s * pieces) * 32 + lane;
+          const int q = q0 + j * kMakerWarps, st = stage_of(q), s = q - st * a.S, x = st * 32 + lane;
 #pragma unroll
           for (int i = 0; i < 8; ++i) v[j][i] = 0.0f;
           br[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          if (s < a.S && x < rows) {
+          if (q < units && x < rows) {
             load_x8(a, s, k0 + x * 8, v[j]);
             if (a.transform) br[j] = __ldg(reinterpret_cast<const float4*>(a.B + (size_t)(k0 >> 3) * 4 + x * 4));
           }
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int s = (p0 + j * kMakerWarps) / pieces;
+          const int q = q0 + j * kMakerWarps;
           float m = 0.0f;
 #pragma unroll
           for (int i = 0; i < 8; ++i) m = fabsf(v[j][i]) <= 3.402823466e38f ? fmaxf(m, fabsf(v[j][i])) : m;
@@ -337,53 +373,45 @@ __global__ void __launch_bounds__(kThreads, 1)
             m *= 4.0f * a.a_norm * fmaxf(fmaxf(fabsf(br[j].x), fabsf(br[j].y)), fmaxf(fabsf(br[j].z), fabsf(br[j].w)));
           // (not negative: ordered as bits)
           const unsigned bits = __reduce_max_sync(0xffffffffu, __float_as_uint(fminf(m, 3.402823466e38f)));
-          if (lane == 0 && s < a.S) atomicMax(&s_amax[s], bits);
+          if (lane == 0 && q < units) atomicMax(&s_amax[q - stage_of(q) * a.S], bits);
         }
       }
       asm volatile("bar.sync 1, %0;" ::"n"(kMakers) : "memory");
-      if (id < a.S) s_xf[id] = e8m0_value((uint32_t)(127 + digit_exponent(__uint_as_float(s_amax[id])))) * 0.00390625f;
+      if (tid < a.S) s_xf[tid] = e8m0_value((uint32_t)(127 + digit_exponent(__uint_as_float(s_amax[tid])))) * 0.00390625f;
     }
-    // Items are rows in the order of the stages, within a stage token after token: 32 rows (8 blocks) of
-    // each.  A warp's items are one token's, and the rows of a block meet in its shuffles.
-    const int stage_rows = 32, items = a.S * rows;
-    const int whole = (rows >> 5) * stage_rows * a.S;  // items of whole stages; the last may have fewer rows
-    auto place = [&](int item, int& s, int& x) {      // token and row of an item
-      if (item < whole) {
-        const int st = item / (stage_rows * a.S), r = item - st * (stage_rows * a.S);
-        s = r >> 5;
-        x = st * stage_rows + (r & 31);
-      } else {
-        const int left = rows & 31, r = item - whole;
-        s = r / left;
-        x = (rows & ~31) + r - s * left;
-      }
-    };
     int pass = 0;
-    for (int i0 = 0; i0 < items; i0 += kMakers, ++pass) {
-      const int item = i0 + id;
-      const bool live = item < items;
-      int s = 0, x = 0;
-      if (live) place(item, s, x);
-      const int b = x & 3, blk = x >> 2, k = k0 + blk * 32;
+    for (int q = warp; q < units; q += kMakerWarps, ++pass) {
+      const int st = stage_of(q), s = q - st * a.S;
+      const int x = st * 32 + lane, b = lane & 3, blk = x >> 2, k = k0 + blk * 32;
       float y[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) y[i] = 0.0f;
-      if (live) {
+      if (x < rows) {  // (a last stage with fewer rows has zeros behind them, which no product reads)
         if (a.transform) {
-          float u[8];
+          float2 u[4], y2[4];
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             float v[8];
             load_x8(a, s, k + r * 8, v);
             const float w = __ldg(a.B + (size_t)(k >> 5) * 16 + r * 4 + b);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) u[c] = r == 0 ? w * v[c] : fmaf(w, v[c], u[c]);
+            for (int c = 0; c < 4; ++c)
+              u[c] = r == 0 ? make_float2(w * v[2 * c], w * v[2 * c + 1])
+                            : fma2(make_float2(w, w), make_float2(v[2 * c], v[2 * c + 1]), u[c]);
           }
 #pragma unroll
-          for (int d = 0; d < 8; ++d) {
-            y[d] = u[0] * a.A[d];
+          for (int c = 0; c < 8; ++c) {
+            const float f = (c & 1) ? u[c >> 1].y : u[c >> 1].x;
 #pragma unroll
-            for (int c = 1; c < 8; ++c) y[d] = fmaf(u[c], a.A[c * 8 + d], y[d]);
+            for (int d = 0; d < 4; ++d) {
+              const float2 m = make_float2(a.A[c * 8 + 2 * d], a.A[c * 8 + 2 * d + 1]);
+              y2[d] = c == 0 ? make_float2(f * m.x, f * m.y) : fma2(make_float2(f, f), m, y2[d]);
+            }
+          }
+#pragma unroll
+          for (int d = 0; d < 4; ++d) {
+            y[2 * d] = y2[d].x;
+            y[2 * d + 1] = y2[d].y;
           }
         } else {
           load_x8(a, s, k + b * 8, y);
@@ -406,6 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         byte = (uint8_t)(finite ? e + 127 : 255);
       }
+      // (Digits of a block that is not finite are any: its scale is NaN.)
       // Fixed point: adding 1.5 * 2^23 leaves the rounded integer (at most 2^22) in the low bits, and four
       // of every digit make the digits -4 .. 3 the fields 0 .. 7.
       constexpr uint32_t kFours = 04444444444u & ((1u << (3 * kParts)) - 1);
@@ -414,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t v[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        v[i] = __float_as_uint(fmaf(finite ? y[i] * inv : 0.0f, kUnit, 12582912.0f)) + (kFours - 0x4B400000u);
+        v[i] = __float_as_uint(fmaf(y[i] * inv, kUnit, 12582912.0f)) + (kFours - 0x4B400000u);
       // Two numbers to a register: the last five digits (15 bits), and of eight the first four.
       constexpr int kLow = kParts == 5 ? 5 : 4;
       uint32_t low[4], high[4];
@@ -423,27 +452,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         low[i] = __byte_perm(v[2 * i], v[2 * i + 1], 0x5410);
         high[i] = __byte_perm(v[2 * i] >> (3 * kLow), v[2 * i + 1] >> (3 * kLow), 0x5410);
       }
-      const uint32_t turn = blk & 7;
-      uint8_t* dst = s_x + (size_t)(blk >> 3) * (a.n * 128) + b * 4;
+      // Column r = kP * kSp + s: kSp is a power of two above s, so the digit's part of the addresses is constant.
+      uint8_t* dst = s_x + (size_t)st * (a.n * 128) + b * 4 + s * 128;
+      const uint32_t turn = (uint32_t)((blk ^ s) & 7) << 4;
       // Scale byte of column r: four scale columns to a tile, row r % 32, then r / 32, then the scale column.
       const int col = kNv ? blk * 2 + (b >> 1) : blk;
-      uint8_t* sc = s_sx + (col >> 2) * kSfAtom + (col & 3);
-      const bool writes_scale = live && (kNv ? (b & 1) == 0 : b == 0);
+      uint8_t* sc = s_sx + (col >> 2) * kSfAtom + (col & 3) + s * 16;
+      const bool writes_scale = kNv ? (b & 1) == 0 : b == 0;
       for_digits<kParts>([&](auto p_tag) {
-        constexpr int kP = decltype(p_tag)::value;
-        const uint32_t r = kP * kSp + s;
+        constexpr int kP = decltype(p_tag)::value, kR = kP * kSp;
         uint32_t w;
         if constexpr (kParts - kP <= kLow)
           w = digit_codes<3 * (kParts - 1 - kP)>(low);
         else
           w = digit_codes<3 * (kParts - 1 - kP - kLow)>(high);
-        if (live) *reinterpret_cast<uint32_t*>(dst + r * 128 + ((turn ^ (r & 7)) << 4)) = w;
-        if (writes_scale) sc[(r & 31) * 16 + (r >> 5) * 4] = byte;
+        *reinterpret_cast<uint32_t*>(dst + kR * 128 + (turn ^ ((kR & 7) << 4))) = w;
+        if (writes_scale) sc[(kR & 31) * 16 + (kR >> 5) * 4] = byte;
       });
       fence_proxy_async_smem();  // the tensor core reads shared memory through the asynchronous proxy
       __syncwarp();
       if (lane == 0) mbar_arrive(&made[pass]);
     }
+    if (lane == 0 && pass * kMakerWarps < units) mbar_arrive(&made[pass]);  // (a last pass without a unit for this warp)
 
     if (warp < 4) {
       // ------------------------------ epilogue ------------------------------
