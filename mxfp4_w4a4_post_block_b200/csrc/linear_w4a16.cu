@@ -23,7 +23,13 @@
 // MMAs per stage into one of two accumulators, four drain the other.  Sixteen warps make the digits,
 // stage after stage, so the first tile's products begin with the first stage's.  The CTAs of a cluster
 // split K where the digits would not fit otherwise or where it balances the tiles over the SMs
-// (launch_cfg); their sums meet in distributed shared memory, rank after rank.
+// (launch_cfg); each sends its sums straight to the CTA that adds their rows, rank after rank (one way
+// through distributed shared memory; fetching them after a barrier of the cluster took 1 to 2 us more).
+//
+// What bounds it: at one tile per CTA the chain of launch, digits (1.4 us per unit of a warp), products
+// and exchange; with many the stream of weights.  Measured: one token x 4096 x 4096 5.7 us (1.5 TB/s; an
+// empty kernel's launch takes 2.5), four x 4096 x 24576 13.0 us (4.1 TB/s), seven x 12288 x 4096 NVFP4
+// with fp32 out 12.5 us (2.3 TB/s), 16 x 4096 x 24576 22 us.
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
@@ -104,14 +110,22 @@ __device__ __forceinline__ uint32_t digit_codes(const uint32_t (&v)[4]) {
   return __byte_perm(kNeg, kPos, sel) | __byte_perm(kNeg << 4, kPos << 4, sel >> 16);
 }
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
-}
-
-__device__ __forceinline__ void mbar_arrive_release_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+// Writes kN floats to a peer's shared memory and counts their bytes on its barrier.
+template <int kN>
+__device__ __forceinline__ void push_cluster(uint32_t addr, const float* v, uint32_t bar) {
+  if constexpr (kN == 1)
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(addr),
+                 "r"(__float_as_uint(v[0])), "r"(bar)
+                 : "memory");
+  else if constexpr (kN == 2)
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::"r"(addr),
+                 "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(bar)
+                 : "memory");
+  else
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr),
+                 "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
+                 "r"(__float_as_uint(v[3])), "r"(bar)
+                 : "memory");
 }
 
 // mbar_wait_warp with an acquire at cluster scope.
@@ -184,8 +198,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* s_x = s_w + a.ring * kStageBytes;                               // [stage][column] digits
   uint8_t* s_sw = s_x + (size_t)a.max_stages * a.n * 128;                  // [ring] weight scale tiles
   uint8_t* s_sx = s_sw + a.ring * kSfBytes;                                // digit scale tiles
-  float* s_sums = reinterpret_cast<float*>(s_sx + a.max_stages * kSfBytes);  // [2][kSp][128]
-  float* s_xf = s_sums + 2 * kRows * kSp;                                  // [16] NVFP4: each token's unit
+  float* s_sums = reinterpret_cast<float*>(s_sx + a.max_stages * kSfBytes);  // [2][rank][row][kSp]
+  float* s_xf = s_sums + 2 * (kRows + 8) * kSp;                                  // [16] NVFP4: each token's unit
   unsigned* s_amax = reinterpret_cast<unsigned*>(s_xf + 16);               // [16]
   uint64_t* full = reinterpret_cast<uint64_t*>(s_amax + 16);
   uint64_t* empty = full + kMaxRing;
@@ -213,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
       mbar_init(&acc_empty[i], 4);
-      mbar_init(&sums_ready[i], 4 * csize);
+      mbar_init(&sums_ready[i], 1);
     }
     fence_barrier_init();
   }
@@ -258,7 +272,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------ scale copies and MMAs ------------------------------
     // One thread's copies and MMAs run in order.  (Another warp issuing the copies a stage ahead, as in
     // the GEMMs with wide tiles, costs a commit and a barrier per stage: 9.8 instead of 8.4 us for one
-    // tile of K = 4096.)  The loop runs warp-wide (warp-uniform state) with one elected lane issuing.
+    // tile of K = 4096; the same thread issuing them ahead of the last stage's MMAs 20 instead of 15 us for
+    // four tokens x 4096 x 24576.)  It is that thread's own instructions that take the time, so the loop is
+    // its alone, without votes, and has straight-line code for whole stages.
     const bool issuer = elect_one();
     if (issuer) {
     const int whole_stages = a.N / kStageK;
@@ -520,8 +536,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int s = 0; s < kSp; ++s) sum[s] *= unit[s];
         const int r = 32 * quad + lane, m = tile * kRows + r;
-        auto store = [&](int s, float v) {
-          const size_t o = (size_t)s * a.ldo + m;
+        auto store = [&](int s, int at, float v) {
+          const size_t o = (size_t)s * a.ldo + at;
           if (a.out_bf16)
             static_cast<uint16_t*>(a.out)[o] = (uint16_t)pack_bf16x2(v * alpha, 0.0f);
           else
@@ -530,28 +546,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (csize == 1) {
 #pragma unroll
           for (int s = 0; s < kSp; ++s)
-            if (s < a.S && m < a.M) store(s, sum[s]);
+            if (s < a.S && m < a.M) store(s, m, sum[s]);
         } else {
-          float* sums = s_sums + buf * (kRows * kSp);
+          // Rank c adds the rows from c * share on, rank after rank.  A warp sends a tile's sums only after the
+          // last one's have all come, which every warp of the cluster sends after it has read the one before:
+          // so two buffers do.
+          const int share = (kRows + (int)csize - 1) / (int)csize, mine = min(share, kRows - share * (int)crank);
+          float* sums = s_sums + buf * ((kRows + 8) * kSp);
+          if (tid == 0) mbar_arrive_expect_tx(&sums_ready[buf], csize * (uint32_t)(mine * kSp * 4));
+          const int to = r / share;
+          const uint32_t bar = mapa_shared(smem_u32(&sums_ready[buf]), (uint32_t)to);
+          const uint32_t dst = mapa_shared(smem_u32(sums + ((int)crank * share + r - to * share) * kSp), (uint32_t)to);
+          constexpr int kVec = kSp < 4 ? kSp : 4;
 #pragma unroll
-          for (int s = 0; s < kSp; ++s) sums[s * kRows + r] = sum[s];
-          __syncwarp();
-          if (lane == 0)
-            for (uint32_t c = 0; c < csize; ++c) mbar_arrive_release_cluster(mapa_shared(smem_u32(&sums_ready[buf]), c));
+          for (int s = 0; s < kSp; s += kVec) push_cluster<kVec>(dst + s * 4, sum + s, bar);
           if (!mbar_wait_warp_cluster(&sums_ready[buf], (it >> 1) & 1)) {
             if (lane == 0) set_error(a.err, kErrDataTimeout);
             break;
           }
-          // Rank c adds and writes every csize-th token's row, rank after rank.
-          for (int s = (int)crank; s < a.S; s += (int)csize) {
+          for (int x = tid; x < mine * a.S; x += 128) {
+            const int s = x / mine, row = x - s * mine, out_m = tile * kRows + (int)crank * share + row;
             float v[8];
 #pragma unroll
-            for (uint32_t c = 0; c < 8; ++c)
-              v[c] = c < csize ? ld_cluster_f32(mapa_shared(smem_u32(sums + s * kRows + r), c)) : 0.0f;
+            for (int c = 0; c < 8; ++c) v[c] = c < (int)csize ? sums[(c * share + row) * kSp + s] : 0.0f;
             float total = v[0];
 #pragma unroll
             for (int c = 1; c < 8; ++c) total += v[c];
-            if (m < a.M) store(s, total);
+            if (out_m < a.M) store(s, out_m, total);
           }
         }
       }
@@ -560,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before_sync();
   __syncthreads();
-  if (csize > 1) cluster_sync_all();  // peers may still read this CTA's sums
+  if (csize > 1) cluster_sync_all();  // peers may still send sums to this CTA
   if (warp == kMmaWarp) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, 512);
@@ -575,7 +596,7 @@ bool plan(W4Args& a, int sp, int csize, size_t* smem) {
   constexpr int kAtoms = kNv ? 4 : 2;
   a.max_stages = (a.stages + csize - 1) / csize;
   a.n = (a.parts * sp + 15) & ~15;
-  const size_t fixed = (size_t)a.max_stages * (a.n * 128 + kAtoms * kSfAtom) + 2 * (size_t)kRows * sp * 4 + 32 * 4 +
+  const size_t fixed = (size_t)a.max_stages * (a.n * 128 + kAtoms * kSfAtom) + 2 * (size_t)(kRows + 8) * sp * 4 + 32 * 4 +
                        (2 * kMaxRing + 6 + kMaxPasses) * 8 + 16 + 1024;
   a.acc_stride = (a.n + 31) & ~31;
   a.t_sx = 2 * a.acc_stride;
@@ -615,14 +636,15 @@ cudaError_t launch_cfg(const LinearW4A16Launch& L, W4Args& a, cudaStream_t strea
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   // Cluster size along K, by the time that it would take (us; fitted to sizes 1 to 8 for 1 to 16 tokens,
-  // K = 4096 and 12288, 4096 to 24576 out-features):
-  //   * rounds of tiles over the clusters that run at the same time (clusters do not cross GPCs), each
-  //     0.37 per stage with every SM streaming, or 0.5 per CTA that exchanges sums where that is longer;
-  //   * the digits, 0.007 per stage, token and digit, which the CTAs of a cluster share;
-  //   * 1 for a cluster's start.
-  // Four tokens x 4096 x 24576: 17.1 us alone, 14.9 in pairs, 19.0 in threes; one x 4096 x 4096 (32
-  // tiles): 9.3 in pairs, 7.2 in fours, 10.7 in eights; one x 4096 x 18944 (one tile per SM): 11.3 alone,
-  // 12.4 in pairs.
+  // K = 512 to 12288, 1024 to 24576 out-features; its choices are 1 % above the best on average):
+  //   * rounds of tiles over the clusters that run at the same time (clusters do not cross GPCs), each 0.37
+  //     per stage with every SM streaming, a last one less in proportion, but 0.1; and 0.02 per CTA that
+  //     exchanges sums;
+  //   * the digits, 0.01 per stage, token and digit, which the CTAs of a cluster share;
+  //   * 0.6 for a cluster's start.
+  // Four tokens x 4096 x 24576: 14.5 us alone, 13.1 in pairs, 14.6 in threes; one x 4096 x 4096 (32
+  // tiles): 6.0 in pairs, 5.7 in fours, 6.0 in eights; one x 4096 x 18944 (one tile per SM): 10.2 alone,
+  // 10.9 in pairs; 16 x 4096 x 4096: 16.3 in pairs, 11.6 in fours, 10.7 in eights.
   static int active[64][9] = {};
   int csize = 0;
   size_t smem = 0;
@@ -640,10 +662,10 @@ cudaError_t launch_cfg(const LinearW4A16Launch& L, W4Args& a, cudaStream_t strea
       }
       active[dev][c] = n < 1 ? 1 : n;
     }
-    const int rounds = (a.tiles + active[dev][c] - 1) / active[dev][c];
-    const float round = 0.37f * a.max_stages;
-    const float t = rounds * (c > 1 && round < 0.5f * c ? 0.5f * c : round) + 0.007f * a.max_stages * a.S * kParts +
-                    (c > 1 ? 1.0f : 0.0f);
+    const int full = a.tiles / active[dev][c], rest = a.tiles - full * active[dev][c];
+    float t = a.max_stages * (0.37f * full + 0.01f * a.S * kParts);
+    if (rest > 0) t += a.max_stages * std::fmax(0.1f, 0.37f * rest / active[dev][c]);
+    if (c > 1) t += 0.6f + 0.02f * c * (full + (rest > 0 ? 1 : 0));
     if (csize == 0 || t < best) {
       csize = c;
       best = t;
