@@ -701,7 +701,8 @@ BATQ_API batq_status batq_attn_kv8_workspace_size(int max_q_len, int q_heads, in
  * bf16 queries lose nothing down to 2^-13 of the largest of their 32 head dims,
  * fp32 queries keep 12 bits, and those products are rounded to 2^-20 of the
  * largest among their 32 tokens.  The split of the work depends only on the
- * lengths, so results repeat bit for bit.  Non-finite queries give NaN.
+ * lengths, so results repeat bit for bit.  Non-finite queries, and scores
+ * beyond fp32's range, give NaN.
  * workspace: device, 16-byte aligned; calls that may overlap need one each.
  * Errors: BATQ_ERR_INVALID_ARG (softmax_scale not finite), BATQ_ERR_SHAPE,
  * BATQ_ERR_ALIGNMENT, BATQ_ERR_WORKSPACE, BATQ_ERR_ARCH, BATQ_ERR_CUDA.

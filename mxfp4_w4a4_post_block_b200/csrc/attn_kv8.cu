@@ -424,15 +424,47 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
                 s[mk][n][e] = -INFINITY;
               }
         }
-        float m_new[2];
+        float f0[2], f1[2], base[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float x0 = fmaf(fmaxf(s[0][n][e], s[0][n][2 + e]), rf[n][e] * h0.x, h0.y);
-          const float x1 = fmaf(fmaxf(s[1][n][e], s[1][n][2 + e]), rf[n][e] * h1.x, h1.y);
+          f0[e] = rf[n][e] * h0.x;
+          f1[e] = rf[n][e] * h1.x;
+          base[e] = 0.0f;
+        }
+        // The maximum is taken of rounded scores, the weights' differences of exact ones: so scores that may pass
+        // 2^21 (the products' sums stay below 2^32) are rounded first, and counted from the tile's largest.
+        if (__any_sync(0xffffffffu, fmaxf(fmaxf(f0[0], f0[1]), fmaxf(f1[0], f1[1])) > 0x1p-11f)) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int q = 0; q < 4; q += 2) {
+              s[0][n][q + e] = s[0][n][q + e] == -INFINITY ? -INFINITY : s[0][n][q + e] * f0[e];
+              s[1][n][q + e] = s[1][n][q + e] == -INFINITY ? -INFINITY : s[1][n][q + e] * f1[e];
+            }
+            float mx = fmaxf(fmaxf(s[0][n][e], s[0][n][2 + e]), fmaxf(s[1][n][e], s[1][n][2 + e]));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            base[e] = mx > -INFINITY ? mx : 0.0f;
+#pragma unroll
+            for (int q = 0; q < 4; q += 2) {
+              s[0][n][q + e] -= base[e];
+              s[1][n][q + e] -= base[e];
+            }
+            f0[e] = f1[e] = 1.0f;
+          }
+        }
+        float m_new[2], local[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float x0 = fmaf(fmaxf(s[0][n][e], s[0][n][2 + e]), f0[e], h0.y);
+          const float x1 = fmaf(fmaxf(s[1][n][e], s[1][n][2 + e]), f1[e], h1.y);
           float mx = fmaxf(x0, x1);
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-          m_new[e] = max3(m[n][e], mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+          local[e] = mx;
+          m_new[e] = fmaxf(m[n][e], mx + base[e]);
         }
         if (__any_sync(0xffffffffu, m_new[0] > m[n][0] || m_new[1] > m[n][1])) {
           float alpha[2];
@@ -450,9 +482,11 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
         float b0[2], b1[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float base_e = m[n][e] == -INFINITY ? 0.0f : m[n][e] - (float)kBias;
-          b0[e] = h0.y - base_e;
-          b1[e] = h1.y - base_e;
+          // -m + kBias for scores counted from `base`.
+          const float from = base[e] == 0.0f ? m[n][e] : local[e] - ((local[e] + base[e]) - m[n][e]);
+          const float less = m[n][e] == -INFINITY ? 0.0f : from - (float)kBias;
+          b0[e] = h0.y - less;
+          b1[e] = h1.y - less;
         }
 #pragma unroll
         for (int mk = 0; mk < 2; ++mk) {
@@ -460,7 +494,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
           float p[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            p[e] = ex2(fmaf(s[mk][n][e], rf[n][e & 1] * hh.x, mk == 0 ? b0[e & 1] : b1[e & 1]));
+            p[e] = ex2(fmaf(s[mk][n][e], mk == 0 ? f0[e & 1] : f1[e & 1], mk == 0 ? b0[e & 1] : b1[e & 1]));
             if (!kWhole && ((masked >> (4 * mk + e)) & 1u))
               p[e] = 0.0f;  // (a NaN scale is not for this row's sum either)
             else

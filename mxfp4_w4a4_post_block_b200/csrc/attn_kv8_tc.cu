@@ -48,7 +48,7 @@ constexpr int kUnits = 5;                // scales that parts and digits count i
 constexpr int kSfAtom = 512;
 constexpr int kMeta = 8;                 // tiles whose page factors are kept
 constexpr float kWeightUnit = 32.0f;     // weights count 2^-5: 20 bits, and the digits' codes 2^-25
-constexpr float kNoRef = -1.0e30f;       // no key seen yet
+constexpr float kNoRef = -3.0e38f;       // no key seen yet
 constexpr float kRise = 48.0f;           // exponent that the accumulators may grow past their reference
 constexpr float kFarExp = 48.0f;         // V exponents up to it take their sums from the weights
 constexpr float kLowExp = -48.0f;        // V exponents below it do not lower the reference
@@ -95,10 +95,14 @@ __device__ __forceinline__ float redux_max(float v) {
   return r;
 }
 
-__device__ __forceinline__ void group_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ void group_sync(int id) {
+  __syncwarp();
+  asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory");
+}
 // Whether any thread of the group says so.
 __device__ __forceinline__ bool group_any(int id, bool v) {
   uint32_t r;
+  __syncwarp();
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
@@ -111,6 +115,7 @@ __device__ __forceinline__ bool group_any(int id, bool v) {
 }
 template <int kThreads>
 __device__ __forceinline__ void groups_sync() {
+  __syncwarp();
   asm volatile("bar.sync 3, %0;" ::"n"(kThreads) : "memory");
 }
 
@@ -537,7 +542,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
       for (int k = 0; k < kMine; ++k) {
         const int r = warp + kWarps * k;
         float* v = qv[k];
-        const float f = copysignf(e8m0_value((uint32_t)(127 - qe[k])), a.scale_log2);  // the scores' factor stays positive
+        // (the scores' factor stays positive; what lies 2^119 below the largest has no scale, and counts as zero)
+        const float f = qe[k] - top_e < -119 ? 0.0f : copysignf(e8m0_value((uint32_t)(127 - qe[k])), a.scale_log2);
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = fabsf(v[i]) <= 3.402823466e38f ? v[i] * f : __uint_as_float(0x7FC00000u);
 #pragma unroll
@@ -659,15 +665,39 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
           }
           __syncwarp();
         };
+        // The exponents are taken of rounded scores, the weights' differences of exact ones: so scores that may pass
+        // 2^21 (|x| < 2^24) are rounded first, and counted from each row's largest, `base`.
+        float base[kHeld];
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k) base[k] = 0.0f;
+        if (__any_sync(0xffffffffu, fs > 0.125f)) {
+#pragma unroll
+          for (int r = 0; r < kLive; ++r) x[r] *= fs;
+          fs = 1.0f;
+          largest(0.0f, nb_of, base);
+#pragma unroll
+          for (int k = 0; k < kHeld; ++k) {
+            base[k] = base[k] > kNoRef ? base[k] : 0.0f;
+            if (lane + 32 * k < kLive) nb_of[lane + 32 * k] = base[k];
+          }
+          __syncwarp();
+#pragma unroll
+          for (int r = 0; r < kLive; ++r) x[r] -= nb_of[r];
+          __syncwarp();
+        }
         largest(fmaxf(f.y, kLowExp), mx_of + w4 * kLive, held);
 #pragma unroll
-        for (int k = 0; k < kHeld; ++k) weights[k] = held[k];
+        for (int k = 0; k < kHeld; ++k) {
+          weights[k] = held[k];
+          held[k] += base[k];
+        }
         if (__any_sync(0xffffffffu, named && f.y < kLowExp)) largest(f.y, nb_of, weights);
         bool outgrown = bad;
 #pragma unroll
         for (int k = 0; k < kHeld; ++k) {
           const int r = lane + 32 * k;
           if (r < kLive) {
+            mx_of[w4 * kLive + r] = held[k];
             nb_of[r] = weights[k] > kNoRef ? 20.0f - weights[k] : 0.0f;
             outgrown |= held[k] > ref_of[r] + kRise;
           }
@@ -682,7 +712,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
             next[k] = kNoRef;
             if (r < kLive) {
               const float top =
-                  ceilf(fmaxf(fmaxf(mx_of[r], mx_of[kLive + r]), fmaxf(mx_of[2 * kLive + r], mx_of[3 * kLive + r])));
+                  fmaxf(fmaxf(mx_of[r], mx_of[kLive + r]), fmaxf(mx_of[2 * kLive + r], mx_of[3 * kLive + r]));
               const float ref = ref_of[r];
               next[k] = top > ref + kRise ? top : ref;
               if (w4 == 0) chg_of[r] = ref == kNoRef || next[k] == ref ? 1.0f : ex2(ref - next[k]);
@@ -720,7 +750,9 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
         for (int k = 0; k < kHeld; ++k) {
           const int r = lane + 32 * k;
           if (r < kLive) {
-            const float rise = weights[k] > kNoRef ? fminf(fmaxf(weights[k] - ref_of[r], -111.0f), kRise) : 0.0f;
+            const float rise =
+                weights[k] > kNoRef ? fminf(fmaxf(weights[k] + base[k] - ref_of[r], -111.0f), kRise) : 0.0f;
+            mx_of[w4 * kLive + r] = base[k] - ref_of[r];
             fac_of[r] = ex2(rise - 20.0f);
             uint8_t* sf = s_sfp + buf * kSfAtom + w4;
             if constexpr (C::kStacked) {
@@ -741,7 +773,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
         if (__any_sync(0xffffffffu, named && fabsf(f.y) > kFarExp)) {
           unscale = 0.0f;
 #pragma unroll
-          for (int r = 0; r < kLive; ++r) l[r] += ex2(fmaf(x[r], fs, -ref_of[r]));
+          for (int r = 0; r < kLive; ++r) l[r] += ex2(fmaf(x[r], fs, mx_of[w4 * kLive + r]));
         }
         uint8_t* dst = s_p + buf * C::kPBytes + gtid * 16;
 #pragma unroll

@@ -516,6 +516,55 @@ def test_long_attention_sharp_and_extreme_queries(scale):
     attn_check(out, lse, *c, scale, 1)
 
 
+@pytest.mark.parametrize("D,tokens,G", [(64, 0, 4), (128, 0, 4), (256, 0, 20), (128, 2049, 4), (128, 2049, 20)])
+@pytest.mark.parametrize("mag", [1e3, 1e6, 1e9, 1e15, 1e25])
+def test_attention_scores_beyond_fp32_steps(mag, D, tokens, G):
+    """Scores so large that fp32 holds them only in steps above 1: the largest takes all, of either sign, and ordinary
+    rows beside them keep their softmax."""
+    c = long_table(attn_case(22, 4, 1, G, D, 32, 300, 1, spread=2.0), 32, tokens)
+    q = c[0].view(-1, G, D)
+    q[:, 0] *= mag
+    q[:, 1] = -q[:, 0]
+    out, lse = attn_run(*c, 0.1, 1, out_dtype=F32)
+    attn_check(out, None, *c, 0.1, 1)
+    # one token's values, where the runner-up is clearly behind: 2^-20 of the score, and 40 for the weights
+    k = R.e4m3_value(c[4]) * R.e8m0_value(c[5])[..., None, None]
+    v = R.e4m3_value(c[6]) * R.e8m0_value(c[7])[..., None, None]
+    seen = 0
+    for b in range(len(c[2])):
+        L = int(c[2][b])
+        if c[1][b + 1] == c[1][b] or L < 2:
+            continue
+        ids = c[3][b, :(L + 31) // 32]
+        kk, vv = (a[ids, 0].reshape(-1, D)[:L] for a in (k, v))
+        for h in (0, 1):
+            s = kk @ q[c[1][b], h].double().numpy() * 0.1
+            order = np.sort(s)
+            if order[-1] - order[-2] > 40 + np.abs(s).max() * 2.0 ** -15:
+                want = vv[s.argmax()]
+                got = host(out).reshape(-1, G, D)[c[1][b], h]
+                # the weight's own rounding, and what e^-40 of the others may add
+                assert (np.abs(got - want) <= np.abs(want) * 2.0 ** -10 + np.abs(vv).max() * 2.0 ** -19).all()
+                seen += 1
+    assert seen or mag < 1e6
+
+
+@pytest.mark.parametrize("G", [4, 20])
+def test_long_attention_rows_of_far_magnitudes_share_an_item(G):
+    """A head's queries of 1e30 beside one of 1e-20 and ordinary ones: each row's softmax is its own.  (Queries of
+    1e35 leave the range of fp32 scores: 128 products with keys of up to 448 sum to 5.7e39 > 3.4e38, and the
+    header has NaN for those.)"""
+    c = long_table(attn_case(21, 3, 1, G, 128, 32, 300, 1, spread=0.0), 32)
+    q = c[0].view(-1, G, 128)
+    q[:, 0] *= 1e30
+    q[:, 1] *= 1e-20
+    out, lse = attn_run(*c, 0.1, 1, out_dtype=F32)
+    attn_check(out, None, *c, 0.1, 1)
+    tiny = [c[0].clone()] + c[1:]
+    tiny[0].view(-1, G, 128)[:, 1] = 0.0
+    assert (attn_run(*tiny, 0.1, 1, out_dtype=F32)[0].view(-1, G, 128)[:, 1] - out.view(-1, G, 128)[:, 1]).abs().max() < 1e-6
+
+
 def test_long_attention_masks_leave_rows_empty():
     rng = np.random.default_rng(12)
     page, kv, G, D = 16, 2, 2, 128
