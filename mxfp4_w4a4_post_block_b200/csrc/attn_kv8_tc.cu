@@ -18,9 +18,10 @@
 // The page factors: K's multiplies the scores; V's exponent ev is added to them, w = 2^(x + ev), and the sum
 // takes w 2^-ev.
 //
-// An instruction with few columns costs the reading of its 128 x 32 bytes of K or V (45 clocks), whatever its
-// columns: so up to 16 rows the parts and digits are columns of their own (8 instructions per tile instead of
-// 28; 64 sequences of up to 8192 tokens 139 -> 111 us).
+// An instruction with few columns costs the reading of its 128 x 32 bytes of K or V (45 to 80 clocks), whatever
+// its columns: so the parts and digits are columns of their own, all of them up to 24 rows (8 instructions per
+// tile instead of 28; 64 sequences of up to 8192 tokens 139 -> 111 us, 16 of up to 16000 with 24 rows 47 -> 39),
+// two of them above (16 instructions; 40 rows 68 -> 62 us).
 //
 // Softmax: a thread has one key of the tile and all rows, so a row's largest of a warp's 32 keys is one
 // redux instruction, and its digits of 16 rows are 16 bytes: P is the N-major operand, one store per digit.
@@ -28,13 +29,13 @@
 // A CTA has a load warp (tiles of 128 keys, K and V in turn, a ring of 16 KB slots; page ids read two fetches
 // ahead, their factors one), an MMA warp, and one or two groups of four softmax warps that write the outputs
 // too.  Up to 16 rows two CTAs share an SM; above, two groups take the tiles in turn with accumulators of
-// their own, joined through shared memory (one group: 162 us for what two do in 118, 16 sequences of up to
-// 16000 tokens with five queries of eight heads).  The work list, the runs and the join are attn_kv8.cuh's;
-// an item counts kOver units beside its keys (0 -> 4 and 12: 109 -> 100 us and 86 -> 69 us in those cases).
+// their own, joined through shared memory (one group took 162 us where two took 118, 16 sequences of up to
+// 16000 tokens with 40 rows).  The work list, the runs and the join are attn_kv8.cuh's; an item counts kOver
+// units beside its keys (0 -> 4 and 12: 109 -> 100 us and 86 -> 72 us in those cases).
 //
 // Measured: 64 x up to 8192 tokens, 8 heads of 4 queries: 100 us, 5.9 TB/s; one sequence of 131072: 50 us,
-// 5.4 TB/s; both close to the memory's rate.  16 x up to 16000 tokens with 40 rows: 69 us, where the softmax
-// of 40 rows per key bounds it (memory 20 us).
+// 5.4 TB/s; both close to the memory's rate.  16 x up to 16000 tokens with 40 rows: 62 us, where the chain of
+// a tile bounds it (scores, softmax of 40 rows per key, products; memory 20 us).
 #include "attn_kv8.cuh"
 
 namespace batq {
@@ -44,7 +45,7 @@ constexpr int kTcTile = 128;             // keys per tile
 constexpr int kSlotBytes = kTcTile * 128;
 constexpr int kQParts = 3;               // of queries (two hold bf16's eight bits)
 constexpr int kPParts = 5;               // digits of probabilities
-constexpr int kUnits = 5;                // scales that parts and digits count in: 2^-4i
+constexpr int kUnits = 3;                // scales of V's rows: 2^-8i
 constexpr int kSfAtom = 512;
 constexpr int kMeta = 8;                 // tiles whose page factors are kept
 constexpr float kWeightUnit = 32.0f;     // weights count 2^-5: 20 bits, and the digits' codes 2^-25
@@ -59,29 +60,33 @@ template <int kLive, int kGroups_, int kSlots_, int kCtas_, int kOver_>
 struct TcCfg {
   static constexpr int kOver = kOver_;
   static constexpr int kD = 128, kRows = kLive, kUnit = kTcTile, kGroups = kGroups_, kSlots = kSlots_, kCtas = kCtas_;
-  // Up to 16 rows, the parts of a row are columns of their own, so that an instruction reads its tile of K or V
-  // once for all of them; above, TMEM has no room for that, and they are instructions of their own.
-  static constexpr bool kStacked = kLive <= 16;
-  static constexpr int kNQ = kStacked ? (kQParts * kLive + 15) / 16 * 16 : kLive;  // columns of the instructions
-  static constexpr int kNP = kStacked ? (kPParts * kLive + 15) / 16 * 16 : kLive;
+  // Up to 24 rows, the parts of a row are columns of their own, so that an instruction reads its tile of K or V
+  // once for all of them.  Above, TMEM has room for two of them: K's instructions take the first two parts
+  // together, and V's two digits at a time, in units 2^8 apart.
+  static constexpr bool kStacked = kLive <= 24;
+  static constexpr int kRowsN = kStacked ? kLive : (kLive + 15) / 16 * 16;                    // columns of a part
+  static constexpr int kNQ = kStacked ? (kQParts * kLive + 15) / 16 * 16 : 2 * kRowsN;        // columns of scores
+  static constexpr int kNP = kStacked ? (kPParts * kLive + 15) / 16 * 16 : 2 * kRowsN;        // of accumulators
+  static constexpr int kSumParts = kStacked ? kPParts : 2;                                    // that add up
   static constexpr int kWarps = 4 * kGroups;
   static constexpr int kThreads = 32 * (kWarps + 2);
-  static constexpr int kQBytes = kNQ * 128 * (kStacked ? 1 : kQParts);
-  static constexpr int kPBytes = kNP * 128 * (kStacked ? 1 : kPParts);  // a buffer of P
+  static constexpr int kQBytes = kStacked ? kNQ * 128 : kQParts * kRowsN * 128;
+  static constexpr int kPBytes = kStacked ? kNP * 128 : kPParts * kRowsN * 128;  // a buffer of P
   static constexpr int kQOffset = kSlots * kSlotBytes;
   static constexpr int kPOffset = kQOffset + kQBytes;
   static constexpr int kSfOffset = kPOffset + 2 * kPBytes;     // Q's parts, P's two buffers, the units
-  static constexpr int kMetaOffset = kSfOffset + (kQParts + 2 + kUnits) * kSfAtom;
+  static constexpr int kMetaOffset = kSfOffset + (2 + 2 + kUnits) * kSfAtom;
   static constexpr int kRowOffset = kMetaOffset + kMeta * 8 * 16;
   // Per warp and row: maxima, weights' exponents, sums.  Per group and row: reference, its change.  Per row: keys
   // that it sees, four words of NaN bits.
   static constexpr int kBarOffset = kRowOffset + (3 * kWarps + 2 * kGroups + 5) * kLive * 4;
   static constexpr int kBars = 2 * kSlots + 12;
   static constexpr int kSmemBytes = kBarOffset + kBars * 8 + 16 * 4 + 1024;
+  static constexpr int kQAtoms = kStacked ? 1 : 2;
   // TMEM columns: scores [2], accumulators [kGroups], scales
   static constexpr int kSStride = (kNQ + 31) / 32 * 32, kOStride = (kNP + 31) / 32 * 32;
   static constexpr int kTO = 2 * kSStride, kTUnit = kTO + kGroups * kOStride, kTQ = kTUnit + 4 * (kStacked ? 1 : kUnits),
-                       kTP = kTQ + 4 * (kStacked ? 1 : kQParts);
+                       kTP = kTQ + 4 * kQAtoms;
   static constexpr int kTmem = kTP + 8 <= 256 ? 256 : 512;
   static_assert(kTP + 8 <= 512 && kTmem * kCtas <= 512 && kBarOffset % 8 == 0 && kQBytes % 1024 == 0 && kPBytes % 1024 == 0,
                 "layout");
@@ -173,7 +178,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
   uint8_t* s_q = smem + C::kQOffset;
   uint8_t* s_p = smem + C::kPOffset;
   uint8_t* s_sfq = smem + C::kSfOffset;
-  uint8_t* s_sfp = s_sfq + kQParts * kSfAtom;
+  uint8_t* s_sfp = s_sfq + 2 * kSfAtom;
   uint8_t* s_unit = s_sfp + 2 * kSfAtom;                                 // [kUnits] scales of K's and V's rows
   float4* s_meta = reinterpret_cast<float4*>(smem + C::kMetaOffset);     // [kMeta][8 pages] K scale, V exponent, -, named
   float* s_mx = reinterpret_cast<float*>(smem + C::kRowOffset);          // [kWarps][kLive] exponents of a warp's largest
@@ -220,10 +225,10 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
     s_bad[1] = 0;
     fence_barrier_init();
   }
-  // The rows of K and V have the scales 2^-4i of the parts and digits that they meet.
+  // The rows of K have the scale 1, those of V the unit of the digits that they meet.
   if (tid < 128)
     for (int i = 0; i < kUnits; ++i)
-      reinterpret_cast<uint32_t*>(s_unit + i * kSfAtom)[tid] = 0x7F7F7F7Fu - (uint32_t)i * 0x04040404u;
+      reinterpret_cast<uint32_t*>(s_unit + i * kSfAtom)[tid] = 0x7F7F7F7Fu - (uint32_t)i * 0x08080808u;
   fence_proxy_async_smem();
   if (warp == kWarps + 1) {
     tmem_alloc(tmem_holder, C::kTmem);
@@ -370,8 +375,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
     // before the products with a tile's probabilities.
     const bool issuer = elect_one();
     const int q_parts = q_bf16 ? 2 : kQParts;
-    [[maybe_unused]] const int n_q = (q_parts * kLive + 15) / 16 * 16;
-    const int q_atoms = C::kStacked ? 1 : q_parts;
+    const int n_q = C::kStacked ? (q_parts * kLive + 15) / 16 * 16 : C::kNQ;
+    const int q_atoms = C::kStacked ? 1 : q_parts - 1;
     if (issuer)
       for (int i = 0; i < (C::kStacked ? 1 : kUnits); ++i)
         tc_cp_32x128b_warpx4(tmem + C::kTUnit + 4 * i, sdesc_sf_atom(smem_u32(s_unit + i * kSfAtom)));
@@ -402,18 +407,17 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
             const uint64_t dk = sdesc_kmajor_sw128(smem_u32(smem + slot * kSlotBytes));
             const uint64_t dq = sdesc_kmajor_sw128(smem_u32(s_q));
             const uint32_t t_s = tmem + buf * C::kSStride;
-            if constexpr (C::kStacked) {
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                tc_mma_mxf8(t_s, dk + (uint64_t)(j * 2), dq + (uint64_t)(j * 2), idesc_mxf8(128, n_q, 0, j),
-                            tmem + C::kTUnit, tmem + C::kTQ, j > 0 ? 1u : 0u);
-            } else {
-              for (int part = 0; part < q_parts; ++part)
+            for (int j = 0; j < 4; ++j)
+              tc_mma_mxf8(t_s, dk + (uint64_t)(j * 2), dq + (uint64_t)(j * 2), idesc_mxf8(128, n_q, 0, j),
+                          tmem + C::kTUnit, tmem + C::kTQ, j > 0 ? 1u : 0u);
+            if constexpr (!C::kStacked) {
+              if (q_parts == 3) {  // the third part joins the first one's columns
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                  tc_mma_mxf8(t_s, dk + (uint64_t)(j * 2), dq + (uint64_t)(part * (C::kNQ * 128 >> 4) + j * 2),
-                              idesc_mxf8(128, C::kNQ, 0, j), tmem + C::kTUnit + 4 * part, tmem + C::kTQ + 4 * part,
-                              (part > 0 || j > 0) ? 1u : 0u);
+                  tc_mma_mxf8(t_s, dk + (uint64_t)(j * 2), dq + (uint64_t)((2 * C::kRowsN * 128 >> 4) + j * 2),
+                              idesc_mxf8(128, C::kRowsN, 0, j), tmem + C::kTUnit, tmem + C::kTQ + 4, 1u);
+              }
             }
             tc_commit(&empty[slot]);
             tc_commit(&s_full[buf]);
@@ -440,13 +444,15 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
                             idesc_mxf8(128, C::kNP, 0, j) | kMajors, tmem + C::kTUnit, tmem + C::kTP + 4 * buf,
                             (i >= kGroups || j > 0) ? 1u : 0u);
             } else {
-              for (int digit = 0; digit < kPParts; ++digit)
+#pragma unroll
+              for (int digit = 0; digit < kPParts; digit += 2)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                   tc_mma_mxf8(t_acc, dv + (uint64_t)(j * (32 * 128 >> 4)),
-                              dp + (uint64_t)(digit * (C::kNP * 128 >> 4) + j * (32 * 16 >> 4)),
-                              idesc_mxf8(128, C::kNP, 0, j) | kMajors, tmem + C::kTUnit + 4 * (kPParts - 1 - digit),
-                              tmem + C::kTP + 4 * buf, (i >= kGroups || digit > 0 || j > 0) ? 1u : 0u);
+                              dp + (uint64_t)(digit * (C::kRowsN * 128 >> 4) + j * (32 * 16 >> 4)),
+                              idesc_mxf8(128, (digit + 1 < kPParts ? 2 : 1) * C::kRowsN, 0, j) | kMajors,
+                              tmem + C::kTUnit + 4 * (2 - digit / 2), tmem + C::kTP + 4 * buf,
+                              (i >= kGroups || digit > 0 || j > 0) ? 1u : 0u);
             }
             tc_commit(&empty[slot]);
             tc_commit(&p_empty[buf]);
@@ -506,7 +512,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
         }
       }
     };
-    constexpr bool kEarly = C::kStacked;  // (more rows would spill)
+    constexpr bool kEarly = kLive <= 16;  // (more rows would spill)
     int u = u_begin;
     Piece next = {};
     bool more = next_piece(u, next);
@@ -549,13 +555,13 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
 #pragma unroll
         for (int part = 0; part < kQParts; ++part) {
           const uint32_t c = e4m3x4(v[0], v[1], v[2], v[3]);
-          const int n = part * (C::kStacked ? kLive : C::kNQ) + r;  // row of the operand, or of the parts' operands
+          const int n = part * C::kRowsN + r;  // row of the operand
           *reinterpret_cast<uint32_t*>(s_q + n * 128 + (((lane >> 2) ^ (n & 7)) << 4) + (lane & 3) * 4) = c;
           if ((lane & 7) == 0) {
-            if constexpr (C::kStacked)
-              s_sfq[(n & 31) * 16 + (n >> 5) * 4 + (lane >> 3)] = (uint8_t)max(qe[k] - top_e + 127 - 4 * part, 0);
-            else
-              s_sfq[part * kSfAtom + (r & 31) * 16 + (r >> 5) * 4 + (lane >> 3)] = (uint8_t)max(qe[k] - top_e + 127, 0);
+            const bool third = !C::kStacked && part == 2;
+            const int at = third ? r : n;
+            s_sfq[(third ? kSfAtom : 0) + (at & 31) * 16 + (at >> 5) * 4 + (lane >> 3)] =
+                (uint8_t)max(qe[k] - top_e + 127 - 4 * part, 0);
           }
           const float2 lo = e4m3x2_values(c & 0xFFFFu), hi = e4m3x2_values(c >> 16);
           v[0] = (v[0] - lo.x) * 16.0f;
@@ -583,17 +589,18 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
         tc_fence_after_sync();
         float x[kLive];
         tmem_ld_rows(tmem + buf * C::kSStride + lanes, x);
-        if constexpr (C::kStacked) {
-          float y[kLive];
-          tmem_ld_rows(tmem + buf * C::kSStride + lanes + kLive, y);
-          if (!q_bf16) {
-            float z[kLive];
-            tmem_ld_rows(tmem + buf * C::kSStride + lanes + 2 * kLive, z);
 #pragma unroll
-            for (int r = 0; r < kLive; ++r) y[r] += z[r];
+        for (int c = 0; c < kLive; c += 8) {
+          float y[8];
+          tmem_ld_rows(tmem + buf * C::kSStride + lanes + C::kRowsN + c, y);
+          if (C::kStacked && !q_bf16) {
+            float z[8];
+            tmem_ld_rows(tmem + buf * C::kSStride + lanes + 2 * C::kRowsN + c, z);
+#pragma unroll
+            for (int r = 0; r < 8; ++r) y[r] += z[r];
           }
 #pragma unroll
-          for (int r = 0; r < kLive; ++r) x[r] += y[r];
+          for (int r = 0; r < 8; ++r) x[c + r] += y[r];
         }
         tc_fence_before_sync();
         __syncwarp();
@@ -728,13 +735,14 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
             const int before = g - kGroups;  // the group's last tile: all products so far
             wait(&p_empty[before & 1], (before >> 1) & 1, kErrMmaTimeout);
             tc_fence_after_sync();
-            for (int c = 0; c < (C::kStacked ? kPParts : 1) * kLive; c += 8) {
-              float o[8];
-              tmem_ld_rows(t_o + c, o);
+            for (int part = 0; part < C::kSumParts; ++part)
+              for (int c = 0; c < kLive; c += 8) {
+                float o[8];
+                tmem_ld_rows(t_o + part * C::kRowsN + c, o);
 #pragma unroll
-              for (int r = 0; r < 8; ++r) o[r] *= chg_of[c % kLive + r];
-              tmem_st_8(t_o + c, o);
-            }
+                for (int r = 0; r < 8; ++r) o[r] *= chg_of[c + r];
+                tmem_st_8(t_o + part * C::kRowsN + c, o);
+              }
             asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             tc_fence_before_sync();
 #pragma unroll
@@ -762,7 +770,11 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
                 sf[(n & 31) * 16 + (n >> 5) * 4] = (uint8_t)((int)rise + 127 - 4 * (kPParts - 1 - digit));
               }
             } else {
-              sf[(r & 31) * 16 + (r >> 5) * 4] = (uint8_t)((int)rise + 127);
+#pragma unroll
+              for (int odd = 0; odd < 2; ++odd) {
+                const int n = odd * C::kRowsN + r;
+                sf[(n & 31) * 16 + (n >> 5) * 4] = (uint8_t)((int)rise + 127 + 4 * odd);
+              }
             }
           }
         }
@@ -778,11 +790,11 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
         uint8_t* dst = s_p + buf * C::kPBytes + gtid * 16;
 #pragma unroll
         for (int r0 = 0; r0 < kLive; r0 += 16) {
-          constexpr int kWords = kLive < 16 ? 2 : 4;
-          uint32_t d[kWords][5];
+          uint32_t d[4][5];
 #pragma unroll
-          for (int q = 0; q < kWords; ++q) {
+          for (int q = 0; q < 4; ++q) {
             const int r = r0 + 4 * q;
+            if (r >= kLive) break;
             const float4 nb = *reinterpret_cast<const float4*>(nb_of + r);
             const float4 fac = *reinterpret_cast<const float4*>(fac_of + r);
             const float v0 = ex2(fmaf(x[r], fs, f.y + nb.x)), v1 = ex2(fmaf(x[r + 1], fs, f.y + nb.y)),
@@ -795,17 +807,25 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
                                    __float_as_uint(v2 + 8388608.0f), __float_as_uint(v3 + 8388608.0f)};
             digits4(w, d[q]);
           }
-          if constexpr (kLive >= 16) {
-#pragma unroll
-            for (int digit = 0; digit < kPParts; ++digit)
-              *reinterpret_cast<uint4*>(dst + digit * (kLive * 128) + (r0 / 16) * 2048) =
-                  make_uint4(d[0][digit], d[1][digit], d[2][digit], d[3][digit]);
-          } else {  // two digits of eight rows side by side
+          // Row n of the operand: byte n % 16 of the key's 16 bytes in group n / 16.
+          if constexpr (kLive == 8) {  // two digits of eight rows side by side
 #pragma unroll
             for (int digit = 0; digit < kPParts; digit += 2) {
               const int second = digit + 1 < kPParts ? digit + 1 : digit;  // (the last one's columns are not read)
               *reinterpret_cast<uint4*>(dst + digit * 1024) =
                   make_uint4(d[0][digit], d[1][digit], d[0][second], d[1][second]);
+            }
+          } else {
+#pragma unroll
+            for (int digit = 0; digit < kPParts; ++digit) {
+              const int n = digit * C::kRowsN + r0;
+              if (n % 16 == 0 && r0 + 16 <= kLive) {
+                *reinterpret_cast<uint4*>(dst + n * 128) = make_uint4(d[0][digit], d[1][digit], d[2][digit], d[3][digit]);
+              } else {
+                *reinterpret_cast<uint2*>(dst + n / 16 * 2048 + n % 16) = make_uint2(d[0][digit], d[1][digit]);
+                if (r0 + 16 <= kLive)
+                  *reinterpret_cast<uint2*>(dst + (n + 8) / 16 * 2048 + (n + 8) % 16) = make_uint2(d[2][digit], d[3][digit]);
+              }
             }
           }
         }
@@ -837,14 +857,13 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
         float o[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
         if (any_tile && ok) {
           tmem_ld_rows(t_o + c, o);
-          if constexpr (C::kStacked)
 #pragma unroll
-            for (int digit = 1; digit < kPParts; ++digit) {
-              float more[8];
-              tmem_ld_rows(t_o + digit * kLive + c, more);
+          for (int part = 1; part < C::kSumParts; ++part) {
+            float more[8];
+            tmem_ld_rows(t_o + part * C::kRowsN + c, more);
 #pragma unroll
-              for (int r = 0; r < 8; ++r) o[r] += more[r];
-            }
+            for (int r = 0; r < 8; ++r) o[r] += more[r];
+          }
         }
 #pragma unroll
         for (int r = 0; r < 8; ++r) merge[(c + r) * 128 + gtid] = o[r];
@@ -957,10 +976,15 @@ cudaError_t launch_tc(const AttnKv8Launch& L, cudaStream_t stream) {
 
 cudaError_t launch_attn_kv8_tc(const AttnKv8Launch& L, cudaStream_t stream) {
   const long long rows = (long long)L.max_q_len * (L.q_heads / L.kv_heads);
-  // Up to 16 rows: two CTAs of 107 KB; above, one with two groups.
-  if (rows <= 8) return launch_tc<TcCfg<8, 1, 5, 2, 4>>(L, stream);
-  if (rows <= 16) return launch_tc<TcCfg<16, 1, 4, 2, 4>>(L, stream);
-  if (rows <= 32) return launch_tc<TcCfg<32, 2, 8, 1, 12>>(L, stream);
+  // Rows in steps of 8, since the softmax's time goes with them (40 rows in an item of 48: 71 us for 16 sequences
+  // of up to 16000 tokens instead of 62).  More than 48 go in equal row tiles.  Up to 16 rows two CTAs of 107 KB
+  // share an SM; above, it has one with two groups.
+  const long long tiles = (rows + 47) / 48, per_tile = (rows + tiles - 1) / tiles;
+  if (per_tile <= 8) return launch_tc<TcCfg<8, 1, 5, 2, 4>>(L, stream);
+  if (per_tile <= 16) return launch_tc<TcCfg<16, 1, 4, 2, 4>>(L, stream);
+  if (per_tile <= 24) return launch_tc<TcCfg<24, 2, 8, 1, 12>>(L, stream);
+  if (per_tile <= 32) return launch_tc<TcCfg<32, 2, 8, 1, 12>>(L, stream);
+  if (per_tile <= 40) return launch_tc<TcCfg<40, 2, 8, 1, 12>>(L, stream);
   return launch_tc<TcCfg<48, 2, 8, 1, 12>>(L, stream);
 }
 

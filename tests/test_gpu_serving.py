@@ -449,7 +449,7 @@ def test_long_attention_ragged(B, kv, G, most, q_most, page):
     attn_check(out, lse, *c, 128 ** -0.5, q_most)
 
 
-@pytest.mark.parametrize("G,q_most", [(4, 1), (4, 3), (4, 8), (8, 6)])
+@pytest.mark.parametrize("G,q_most", [(4, 1), (4, 3), (8, 3), (4, 8), (8, 5), (8, 6), (8, 7)])
 @pytest.mark.parametrize("q_dtype,out_dtype", [(F32, F32), (BF, F32), (F32, BF)])
 def test_long_attention_types(q_dtype, out_dtype, G, q_most):
     c = long_table(attn_case(7, 4, 2, G, 128, 16, 500, q_most, q_dtype=q_dtype), 16)
@@ -478,7 +478,7 @@ def test_long_attention_is_split_and_joined(G, q_most):
     assert torch.equal(out, again) and torch.equal(lse, lse2)
 
 
-@pytest.mark.parametrize("G", [4, 20])
+@pytest.mark.parametrize("G", [4, 20, 28, 36, 44])
 @pytest.mark.parametrize("spread", [0.0, 4.0, 12.0])
 def test_long_attention_page_scales_far_apart(spread, G):
     """K and V pages whose scales differ by many powers of two: references move, digits lose the small blocks."""
@@ -635,7 +635,7 @@ def test_attention_scale_zero_weighs_all_tokens_alike(D, G):
     attn_check(out, lse, *c, 0.0, 3)
 
 
-@pytest.mark.parametrize("G", [4, 12])
+@pytest.mark.parametrize("G", [2, 4, 6, 8, 10, 12])
 @pytest.mark.parametrize("page", [16, 64])
 def test_long_attention_nan_does_not_pass_the_mask(page, G):
     rng = np.random.default_rng(13)
