@@ -13,8 +13,11 @@
 // eight 8-element chunks per thread (64 rows of 128) are loaded together and stay in registers from the
 // maximum to the codes; larger blocks are read twice, eight chunks at a time, the second time from L2.
 // (One chunk at a time, each with its own trip to memory: 23.7 us for 8000 rows of 8 x 128 instead of
-// 17.1.)
+// 17.1.)  The maximum is taken of the bits as integers, two bf16 at a time, and values are checked for NaN and
+// infinities only where that maximum shows some (17.2 -> 14.7 us; memory 11.3).  One token of 64 sequences: 4.2 us,
+// the launch and three dependent reads.
 #include <cstdint>
+#include <type_traits>
 
 #include "kernels.h"
 #include "kv8.cuh"
@@ -69,10 +72,27 @@ __device__ __forceinline__ void values8(const Raw8<kBF16>& r, float (&v)[8]) {
   }
 }
 
+// Largest magnitude of eight elements as loaded and `top`, as fp32 bits (without the sign they are ordered as
+// integers; two bf16 at a time).
+template <bool kBF16>
+__device__ __forceinline__ uint32_t max8(const Raw8<kBF16>& r, uint32_t top) {
+  if constexpr (kBF16) {
+    const uint32_t m = __vmaxu2(__vmaxu2(r.q[0].x & 0x7FFF7FFFu, r.q[0].y & 0x7FFF7FFFu),
+                                __vmaxu2(r.q[0].z & 0x7FFF7FFFu, r.q[0].w & 0x7FFF7FFFu));
+    return max(top, max(m << 16, m & 0xFFFF0000u));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      top = max(max(top, max(r.q[i].x & 0x7FFFFFFFu, r.q[i].y & 0x7FFFFFFFu)),
+                max(r.q[i].z & 0x7FFFFFFFu, r.q[i].w & 0x7FFFFFFFu));
+    return top;
+  }
+}
+
 template <bool kBF16>
 __global__ void __launch_bounds__(kThreads, kBF16 ? 9 : 5) k_kv8_append(const Kv8AppendLaunch a) {
   __shared__ int s_seq, s_page;
-  __shared__ float s_amax[kThreads / 32];
+  __shared__ uint32_t s_top[kThreads / 32];
   griddep_wait();
   griddep_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31;
@@ -143,29 +163,45 @@ __global__ void __launch_bounds__(kThreads, kBF16 ? 9 : 5) k_kv8_append(const Kv
   uint8_t* codes = (is_v ? a.v_codes : a.k_codes) + block * ((size_t)a.page_size * D);
   uint8_t* scale = (is_v ? a.v_scales : a.k_scales) + block;
   const int e_old = off0 > 0 ? (int)*scale - 127 : -127;
-  float amax = 0.0f;
+  auto block_max = [&](uint32_t v) {
+    v = __reduce_max_sync(0xffffffffu, v);
+    if (lane == 0) s_top[tid >> 5] = v;
+    __syncthreads();  // the first time also: every thread has the old scale before it is replaced
+    v = s_top[0];
+#pragma unroll
+    for (int i = 1; i < kThreads / 32; ++i) v = max(v, s_top[i]);
+    return v;
+  };
+  const bool kept = chunks <= kPiece * kThreads;  // the rows stay in registers
+  uint32_t top = 0;
   for (int c0 = tid; c0 < chunks; c0 += kPiece * kThreads) {
     if (c0 != tid) load_piece(c0, raw);
 #pragma unroll
-    for (int j = 0; j < kPiece; ++j) {
-      if (c0 + j * kThreads < chunks) {
-        float v[8];
-        values8<kBF16>(raw[j], v);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float m = fabsf(v[i]);
-          amax = m <= 3.402823466e38f ? fmaxf(amax, m) : amax;
-        }
-      }
-    }
+    for (int j = 0; j < kPiece; ++j)
+      if (c0 + j * kThreads < chunks) top = max8<kBF16>(raw[j], top);
   }
+  top = block_max(top);
+  const bool finite = top < 0x7F800000u;
+  if (!finite) {  // the largest of the finite values
+    top = 0;
+    for (int c0 = tid; c0 < chunks; c0 += kPiece * kThreads) {
+      if (!kept) load_piece(c0, raw);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  if (lane == 0) s_amax[tid >> 5] = amax;
-  __syncthreads();  // also: every thread has the old scale before it is replaced
-  amax = s_amax[0];
+      for (int j = 0; j < kPiece; ++j)
+        if (c0 + j * kThreads < chunks) {
+          float v[8];
+          values8<kBF16>(raw[j], v);
 #pragma unroll
-  for (int i = 1; i < kThreads / 32; ++i) amax = fmaxf(amax, s_amax[i]);
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t m = __float_as_uint(v[i]) & 0x7FFFFFFFu;
+            top = m < 0x7F800000u ? max(top, m) : top;
+          }
+        }
+    }
+    __syncthreads();  // s_top has been read
+    top = block_max(top);
+  }
+  const float amax = __uint_as_float(top);
   const int e = max(e_old, block_exponent(amax));
   if (tid == 0) *scale = (uint8_t)(e + 127);
 
@@ -186,20 +222,26 @@ __global__ void __launch_bounds__(kThreads, kBF16 ? 9 : 5) k_kv8_append(const Kv
   }
   const float inv = e8m0_value((uint32_t)max(127 - e, 0));  // 2^-e
   uint8_t* dst = codes + (size_t)off0 * D;
-  for (int c0 = tid; c0 < chunks; c0 += kPiece * kThreads) {
-    if (chunks > kPiece * kThreads) load_piece(c0, raw);  // otherwise still there
+  auto encode = [&](auto checked) {
+    for (int c0 = tid; c0 < chunks; c0 += kPiece * kThreads) {
+      if (!kept) load_piece(c0, raw);
 #pragma unroll
-    for (int j = 0; j < kPiece; ++j) {
-      const int c = c0 + j * kThreads;
-      if (c < chunks) {
-        float v[8];
-        values8<kBF16>(raw[j], v);
+      for (int j = 0; j < kPiece; ++j) {
+        const int c = c0 + j * kThreads;
+        if (c < chunks) {
+          float v[8];
+          values8<kBF16>(raw[j], v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = finite_or_nan(v[i]) * inv;
-        reinterpret_cast<uint2*>(dst)[c] = make_uint2(e4m3x4(v[0], v[1], v[2], v[3]), e4m3x4(v[4], v[5], v[6], v[7]));
+          for (int i = 0; i < 8; ++i) v[i] = (decltype(checked)::value ? finite_or_nan(v[i]) : v[i]) * inv;
+          reinterpret_cast<uint2*>(dst)[c] = make_uint2(e4m3x4(v[0], v[1], v[2], v[3]), e4m3x4(v[4], v[5], v[6], v[7]));
+        }
       }
     }
-  }
+  };
+  if (finite)
+    encode(std::false_type{});
+  else
+    encode(std::true_type{});
 }
 
 }  // namespace

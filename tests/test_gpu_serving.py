@@ -227,6 +227,29 @@ def test_append_token_by_token_and_extremes():
         kc, ks, vc, vs = g
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 64), (256, 128)])
+def test_append_values_that_are_not_finite(D, page, dtype):
+    """NaN and infinities of either sign among a block's rows, alone in a block, and blocks without any."""
+    rng = np.random.default_rng(D)
+    heads, B = 3, 2
+    cu, lens = np.array([0, 2 * page + 3, 2 * page + 9], np.int32), np.array([2 * page + 3, page + 1], np.int32)
+    table = np.arange(6, dtype=np.int32).reshape(B, 3)
+    x = torch.from_numpy(rng.standard_normal((int(cu[-1]), heads, D)).astype(np.float32))
+    x[1, 0, 3], x[page - 1, 0, D - 1], x[0, 0, 0] = float("inf"), float("-inf"), float("nan")
+    x[page:2 * page, 1] = float("nan")
+    x[2 * page + 4, 2, 7] = float("-inf")
+    x = x.to(dtype).reshape(int(cu[-1]), heads * D)
+    kc, ks = R.cache(rng, 6, heads, page, D)
+    vc, vs = R.cache(rng, 6, heads, page, D)
+    kc[4], vc[4] = kc[4] & 0x77, vc[4] & 0x77  # (the second sequence's older rows hold no NaN)
+    kc[3], vc[3] = kc[3] & 0x77, vc[3] & 0x77
+    g = append_run(x.cuda(), x.cuda(), cu, lens, table, kc, ks, vc, vs)
+    xs = x.double().numpy().reshape(-1, heads, D)
+    append_check(xs, cu, lens, table, page, kc, ks, g[0], g[1])
+    append_check(xs, cu, lens, table, page, vc, vs, g[2], g[3])
+
+
 def test_append_drops_what_has_no_place():
     """Unnamed pages, lengths behind the page table, decreasing and outside ranges, fewer tokens than rows."""
     rng = np.random.default_rng(2)
