@@ -95,20 +95,8 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
-// V's page scales ride on the scores: with x_t the score in log2 units and 2^ev(t) the scale of token
-// t's V block, the weights in the matrix instruction are p_t = 2^(x_t + ev(t) - m + kBias), m the
-// running maximum of x + ev, and the sum takes p_t 2^-(ev(t) + kBias) = 2^(x_t - m).  So f16 keeps 11
-// bits of every weight that matters beside the row's largest product of probability and scale (the
-// bias puts that one at 2^15, and f16's smallest step 2^39 below it) however far apart the blocks'
-// scales are, and the accumulators need no unit of their own.  Scales below 2^kMinExp (an all-zero
-// block has 2^-127) ride as 2^kMinExp, which keeps the sum inside fp32, and the rest multiplies the
-// f16 weights.
-constexpr int kBias = 15;
-constexpr int kMinExp = -100;
+// Outputs in the partials count this (attn_kv8.cu has the weights' bias).
 constexpr float kUnbias = 1.0f / 32768.0f;
-__device__ __forceinline__ float v_exponent(int byte) {
-  return byte == 255 ? __uint_as_float(0x7FC00000u) : (float)max(byte - 127, kMinExp);
-}
 
 // Bit 7 of every byte that is an E4M3 NaN (all of its low seven bits set).
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
