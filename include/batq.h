@@ -620,7 +620,8 @@ typedef enum { BATQ_W4_MXFP4 = 0, BATQ_W4_NVFP4 = 1 } batq_w4_format;
  * or 2^-34 of the token's largest); products are exact and summed in fp32.
  * A non-finite x makes all outputs of its token NaN.
  * Errors: BATQ_ERR_INVALID_ARG (also: only one of A_host and B_dev, w_gs_dev
- * with MXFP4), BATQ_ERR_SHAPE (S > 16, N % 64 != 0 or N > 131072, M % 16 != 0),
+ * with MXFP4), BATQ_ERR_SHAPE (S > 16, N % 64 != 0, N > 98304 or
+ * with NVFP4 > 49152, M % 16 != 0),
  * BATQ_ERR_ALIGNMENT, BATQ_ERR_ARCH, BATQ_ERR_CUDA.
  */
 BATQ_API batq_status batq_linear_w4a16(const void* X, batq_dtype x_dtype, int S, int N, int ldx,

@@ -83,7 +83,9 @@ batq_status batq_linear_w4a16(const void* X, batq_dtype x_dtype, int S, int N, i
   if ((A_host == nullptr) != (B_dev == nullptr)) return BATQ_ERR_INVALID_ARG;
   if (w_format != BATQ_W4_MXFP4 && w_format != BATQ_W4_NVFP4) return BATQ_ERR_INVALID_ARG;
   if (w_gs_dev && w_format != BATQ_W4_NVFP4) return BATQ_ERR_INVALID_ARG;
-  if (S < 1 || S > batq::kMaxW4A16Tokens || N < 64 || N % 64 != 0 || N > batq::kMaxW4A16N) return BATQ_ERR_SHAPE;
+  if (S < 1 || S > batq::kMaxW4A16Tokens || N < 64 || N % 64 != 0 ||
+      N > (w_format == BATQ_W4_NVFP4 ? batq::kMaxW4A16NvN : batq::kMaxW4A16N))
+    return BATQ_ERR_SHAPE;
   if (M < 16 || M % 16 != 0 || (long long)M * (N / 32) >= (1LL << 31)) return BATQ_ERR_SHAPE;
   batq_status st = check_rows(X, x_dtype, N, ldx);
   if (st != BATQ_OK) return st;

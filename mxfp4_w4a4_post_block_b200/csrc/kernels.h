@@ -186,7 +186,8 @@ struct LinearW4A16Launch {
   unsigned* err;
 };
 constexpr int kMaxW4A16Tokens = 16;
-constexpr int kMaxW4A16N = 131072;
+// What the digits' scales of one token leave room for in the tensor memory of a cluster of eight.
+constexpr int kMaxW4A16N = 98304, kMaxW4A16NvN = 49152;
 cudaError_t launch_linear_w4a16(const LinearW4A16Launch& L, cudaStream_t stream);
 
 // Products of the ragged row groups of E experts, MXFP4 x MXFP4.

@@ -85,6 +85,18 @@ def test_w4a16_long_rows_split_over_a_cluster(S, N, tr, fmt):
     w4a16_check(w4a16_run(x, A, B, codes, lin, fmt, F32), x, A, B, codes, lin, fmt)
 
 
+@pytest.mark.parametrize("S,N,M,x_dtype,out_dtype,tr,fmt", [
+    (1, 98304, 16, BF, BF, True, "mxfp4"), (16, 98304, 32, BF, F32, False, "mxfp4"), (1, 49152, 48, F32, F32, False, "nvfp4"),
+    (16, 49152, 16, BF, BF, True, "nvfp4"), (16, 28672, 4112, BF, BF, True, "mxfp4"), (9, 16384, 272, BF, F32, True, "nvfp4"),
+    (5, 192, 37888, BF, BF, False, "mxfp4")])
+def test_w4a16_largest_sizes(S, N, M, x_dtype, out_dtype, tr, fmt):
+    """The longest rows, whose tokens go in groups; wide and flat weights; bit for bit twice."""
+    x, A, B, codes, lin, _ = w4a16_case(S, N, M, fmt, x_dtype, tr, S + M)
+    out = w4a16_run(x, A, B, codes, lin, fmt, out_dtype)
+    w4a16_check(out, x, A, B, codes, lin, fmt)
+    assert torch.equal(out, w4a16_run(x, A, B, codes, lin, fmt, out_dtype))
+
+
 def test_w4a16_many_units_and_tensor_scale():
     x, A, B, codes, lin, _ = w4a16_case(2, 768, 24576, "nvfp4", BF, True, 5)
     gs = torch.tensor([37.5], device="cuda")

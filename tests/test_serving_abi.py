@@ -43,6 +43,12 @@ def test_linear_w4a16_refusals(L):
         (2, 0, SHAPE), (2, 17, SHAPE), (3, 250, SHAPE), (3, 0, SHAPE), (3, 131136, SHAPE), (4, 255, SHAPE),
         (11, 100, SHAPE), (11, 0, SHAPE), (14, 127, SHAPE), (0, FAKE + 2, ALIGN), (4, 260, ALIGN), (14, 130, ALIGN),
         (6, FAKE + 4, ALIGN), (8, FAKE + 8, ALIGN), (9, FAKE + 8, ALIGN), (13, FAKE + 4, ALIGN)])
+    for fmt, most in ((0, 98304), (1, 49152)):
+        wide = list(args)
+        wide[7], wide[3], wide[4] = fmt, most + 64, most + 64
+        assert L.batq_linear_w4a16(*wide) == SHAPE
+        wide[3], wide[8] = most, FAKE + 8  # as far as the next refusal
+        assert L.batq_linear_w4a16(*wide) == ALIGN
     nv = list(args)
     nv[7], nv[10] = 1, FAKE + 2
     assert L.batq_linear_w4a16(*nv) == ALIGN
