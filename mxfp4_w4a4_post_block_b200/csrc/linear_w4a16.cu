@@ -144,6 +144,21 @@ __device__ __forceinline__ bool mbar_wait_warp_cluster(uint64_t* bar, uint32_t p
   return __all_sync(0xffffffffu, done != 0) != 0;
 }
 
+// Joins the four epilogue warps; whether all of their threads say so.
+__device__ __forceinline__ bool all_epilogue(bool v) {
+  uint32_t r;
+  __syncwarp();
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, 2, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)v)
+      : "memory");
+  return r != 0;
+}
+
 // f(0), f(1), .. as compile-time numbers.
 template <int kCount, class F, int... kI>
 __device__ __forceinline__ void for_digits_impl(F&& f, std::integer_sequence<int, kI...>) {
@@ -503,9 +518,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       int it = 0;
       for (int tile = cluster; tile < a.tiles; tile += clusters, ++it) {
         const int buf = it & 1;
-        if (!mbar_wait_warp(&acc_full[buf], (it >> 1) & 1)) {
+        bool ok = mbar_wait_warp(&acc_full[buf], (it >> 1) & 1);
+        if (!ok) {
           if (lane == 0) set_error(a.err, kErrMmaTimeout);
-          break;
+          if (csize == 1) break;  // (in a cluster the four warps leave together, below)
         }
         tc_fence_after_sync();
         const uint32_t taddr = tmem + buf * a.acc_stride + ((uint32_t)(32 * quad) << 16);
@@ -548,32 +564,36 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int s = 0; s < kSp; ++s)
             if (s < a.S && m < a.M) store(s, m, sum[s]);
         } else {
-          // Rank c adds the rows from c * share on, rank after rank.  A warp sends a tile's sums only after the
-          // last one's have all come, which every warp of the cluster sends after it has read the one before:
-          // so two buffers do.
+          // Rank c adds the rows from c * share on, rank after rank.  All four warps read the buffer, so they meet
+          // after each tile: then no warp sends a tile's sums before its CTA has read the last one's.  Rank c's
+          // barrier completes for a tile when every CTA's warps that hold rank c's rows have sent it, so after it
+          // every CTA has read the tile before, and two buffers do.
           const int share = (kRows + (int)csize - 1) / (int)csize, mine = min(share, kRows - share * (int)crank);
           float* sums = s_sums + buf * ((kRows + 8) * kSp);
-          if (tid == 0) mbar_arrive_expect_tx(&sums_ready[buf], csize * (uint32_t)(mine * kSp * 4));
-          const int to = r / share;
-          const uint32_t bar = mapa_shared(smem_u32(&sums_ready[buf]), (uint32_t)to);
-          const uint32_t dst = mapa_shared(smem_u32(sums + ((int)crank * share + r - to * share) * kSp), (uint32_t)to);
-          constexpr int kVec = kSp < 4 ? kSp : 4;
+          if (ok) {
+            if (tid == 0) mbar_arrive_expect_tx(&sums_ready[buf], csize * (uint32_t)(mine * kSp * 4));
+            const int to = r / share;
+            const uint32_t bar = mapa_shared(smem_u32(&sums_ready[buf]), (uint32_t)to);
+            const uint32_t dst = mapa_shared(smem_u32(sums + ((int)crank * share + r - to * share) * kSp), (uint32_t)to);
+            constexpr int kVec = kSp < 4 ? kSp : 4;
 #pragma unroll
-          for (int s = 0; s < kSp; s += kVec) push_cluster<kVec>(dst + s * 4, sum + s, bar);
-          if (!mbar_wait_warp_cluster(&sums_ready[buf], (it >> 1) & 1)) {
-            if (lane == 0) set_error(a.err, kErrDataTimeout);
-            break;
+            for (int s = 0; s < kSp; s += kVec) push_cluster<kVec>(dst + s * 4, sum + s, bar);
+            ok = mbar_wait_warp_cluster(&sums_ready[buf], (it >> 1) & 1);
+            if (!ok && lane == 0) set_error(a.err, kErrDataTimeout);
           }
-          for (int x = tid; x < mine * a.S; x += 128) {
-            const int s = x / mine, row = x - s * mine, out_m = tile * kRows + (int)crank * share + row;
-            float v[8];
+          if (ok) {
+            for (int x = tid; x < mine * a.S; x += 128) {
+              const int s = x / mine, row = x - s * mine, out_m = tile * kRows + (int)crank * share + row;
+              float v[8];
 #pragma unroll
-            for (int c = 0; c < 8; ++c) v[c] = c < (int)csize ? sums[(c * share + row) * kSp + s] : 0.0f;
-            float total = v[0];
+              for (int c = 0; c < 8; ++c) v[c] = c < (int)csize ? sums[(c * share + row) * kSp + s] : 0.0f;
+              float total = v[0];
 #pragma unroll
-            for (int c = 1; c < 8; ++c) total += v[c];
-            if (out_m < a.M) store(s, out_m, total);
+              for (int c = 1; c < 8; ++c) total += v[c];
+              if (out_m < a.M) store(s, out_m, total);
+            }
           }
+          if (!all_epilogue(ok)) break;
         }
       }
     }
