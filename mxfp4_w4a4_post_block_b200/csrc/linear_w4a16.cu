@@ -30,6 +30,7 @@
 // and exchange; with many the stream of weights.  Measured: one token x 4096 x 4096 5.7 us (1.5 TB/s; an
 // empty kernel's launch takes 2.5), four x 4096 x 24576 13.0 us (4.1 TB/s), seven x 12288 x 4096 NVFP4
 // with fp32 out 12.5 us (2.3 TB/s), 16 x 4096 x 24576 22 us.
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
@@ -59,7 +60,7 @@ struct W4Args {
   const void* X;
   int x_bf16, S, N, ldx;
   int transform;
-  float A[64], a_norm;        // a_norm: largest column sum of |A|
+  float A[64], a_norm;        // a_norm: four times the largest column sum of |A|
   const float* B;
   const uint8_t* scales;
   const float* gs;
@@ -378,7 +379,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int rows = ((k1 - k0) >> 5) * 4;  // of each token
     if constexpr (kNv) {
       // E4M3 scales span 17 powers of two, so a token's blocks are scaled relative to a bound of its
-      // largest magnitude: |y| <= max |x| |B|_1 |A|_1 over its blocks.
+      // largest magnitude: |y| <= max |x| |B|_1 |A|_1 over its blocks, multiplied in the order that y is (x by B,
+      // then by A), so that it keeps fp32's range where y does.
       // Four units in flight.
       for (int q0 = warp; q0 < units; q0 += 4 * kMakerWarps) {
         float v[4][8];
@@ -401,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 8; ++i) m = fabsf(v[j][i]) <= 3.402823466e38f ? fmaxf(m, fabsf(v[j][i])) : m;
           if (a.transform)
-            m *= 4.0f * a.a_norm * fmaxf(fmaxf(fabsf(br[j].x), fabsf(br[j].y)), fmaxf(fabsf(br[j].z), fabsf(br[j].w)));
+            m = m * fmaxf(fmaxf(fabsf(br[j].x), fabsf(br[j].y)), fmaxf(fabsf(br[j].z), fabsf(br[j].w))) * a.a_norm;
           // (not negative: ordered as bits)
           const unsigned bits = __reduce_max_sync(0xffffffffu, __float_as_uint(fminf(m, 3.402823466e38f)));
           if (lane == 0 && q < units) atomicMax(&s_amax[q - stage_of(q) * a.S], bits);
@@ -459,7 +461,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       int e = digit_exponent(__uint_as_float(finite ? top : 0u));
       if constexpr (kNv) {
         const int e_tok = digit_exponent(__uint_as_float(s_amax[s]));
-        e = max(e, e_tok - 17);
+        // (y and its bound are rounded apart, so y may pass the bound's power of two by its last bits: the digits hold
+        // up to 3.4 * 2^e.)
+        e = min(max(e, e_tok - 17), e_tok);
         const int E = e - e_tok + 8;  // -9 .. 8: the E4M3 power of two
         byte = (uint8_t)(!finite ? 0x7F : E >= -6 ? (E + 7) << 3 : 1 << (E + 9));
       } else {
@@ -708,9 +712,9 @@ cudaError_t launch_fmt(const LinearW4A16Launch& L, cudaStream_t stream) {
   a.transform = L.transform;
   for (int i = 0; i < 64; ++i) a.A[i] = L.A[i];
   for (int d = 0; d < 8; ++d) {
-    float sum = 0.0f;
-    for (int c = 0; c < 8; ++c) sum += std::fabs(L.A[c * 8 + d]);
-    a.a_norm = sum > a.a_norm ? sum : a.a_norm;
+    double sum = 0.0;
+    for (int c = 0; c < 8; ++c) sum += 4.0 * std::fabs(L.A[c * 8 + d]);
+    a.a_norm = std::fmax(a.a_norm, (float)std::fmin(sum, (double)FLT_MAX));
   }
   a.B = L.B;
   a.scales = L.w_scales;
