@@ -701,7 +701,9 @@ BATQ_API batq_status batq_attn_kv8_workspace_size(int max_q_len, int q_heads, in
  * f16, and to 2^-40 of the row's largest.  Head dim 128 with longer tables:
  * bf16 queries lose nothing down to 2^-13 of the largest of their 32 head dims,
  * fp32 queries keep 12 bits, and those products are rounded to 2^-20 of the
- * largest among their 32 tokens.  The split of the work depends only on the
+ * largest among their 32 tokens (2^-60 of the row's largest).  The scales of a
+ * row's pages may lie anywhere in E8M0's range; a token whose probability is
+ * below 2^-126 of the row's largest may count as none.  The split of the work depends only on the
  * lengths, so results repeat bit for bit.  Non-finite queries, and scores
  * beyond fp32's range, give NaN.
  * workspace: device, 16-byte aligned; calls that may overlap need one each.

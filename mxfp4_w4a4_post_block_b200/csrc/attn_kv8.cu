@@ -96,8 +96,9 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 // bits of every weight that matters beside the row's largest product of probability and scale (the
 // bias puts that one at 2^15, and f16's smallest step 2^39 below it) however far apart the blocks'
 // scales are, and the accumulators need no unit of their own.  Scales below 2^kMinExp (an all-zero
-// block has 2^-127) ride as 2^kMinExp, which keeps the sum inside fp32, and the rest multiplies the
-// f16 weights.
+// block has 2^-127) ride as 2^kMinExp, and the rest multiplies the f16 weights.  From the first tile
+// on whose |ev| is beyond kFarExp, a sum has a reference of its own (kFarExp has which) and
+// exponentials of its own; a piece's outputs are brought to that reference at its end.
 constexpr int kBias = 15;
 constexpr int kMinExp = -100;
 __device__ __forceinline__ float v_exponent(int byte) {
@@ -345,6 +346,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
     // This lane's rows: 8 n + 2 t and the next of its warp's; keys of a tile: 16 mk + g and + 8.
     float o[kD / 16][kNT][4];
     float m[kNT][2], l[kNT][2], rf[kNT][2];
+    float lm[kNT][2];  // the sums' reference, where it is not m
+    bool far = false;  // it is not (the same for the warp)
     int lim[kNT][2];
 #pragma unroll
     for (int n = 0; n < kNT; ++n) {
@@ -353,7 +356,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int r = rw * C::kRowsPerWarp + n * 8 + 2 * t + i;
-        m[n][i] = -INFINITY;
+        m[n][i] = lm[n][i] = -INFINITY;
         l[n][i] = 0.0f;
         rf[n][i] = s_rf[r];
         lim[n][i] = min(lim0 + (rt * kRows + r) / a.group, it.s.len);
@@ -416,6 +419,14 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
         }
       }
       release(2 * i);
+      if (!far && fmaxf(fabsf(h0.y), fabsf(h1.y)) > kFarExp) {
+        far = true;
+#pragma unroll
+        for (int n = 0; n < kNT; ++n) {
+          lm[n][0] = m[n][0];
+          lm[n][1] = m[n][1];
+        }
+      }
 
       // Softmax.  The maximum is taken of the raw scores, whose factor is positive.
       uint32_t pb[2][kNT][2];  // P^T: the second product's operand
@@ -478,14 +489,37 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
           float alpha[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            alpha[e] = m_new[e] > m[n][e] ? ex2(m[n][e] - m_new[e]) : 1.0f;
+            const Pow2 change = pow2_of(m_new[e] > m[n][e] ? m[n][e] - m_new[e] : 0.0f);
+            alpha[e] = change.a * change.b;  // (outputs below 2^-126 of the largest product are beyond f16's steps)
             m[n][e] = m_new[e];
-            l[n][e] *= alpha[e];
+            if (!far) l[n][e] = times(l[n][e], change);
           }
 #pragma unroll
           for (int d = 0; d < kD / 16; ++d)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[d][n][e] *= alpha[e & 1];
+        }
+        if (far) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float x0 = fmaf(fmaxf(s[0][n][e], s[0][n][2 + e]), f0[e], near_exponent(h0.y));
+            const float x1 = fmaf(fmaxf(s[1][n][e], s[1][n][2 + e]), f1[e], near_exponent(h1.y));
+            float mx = fmaxf(x0, x1);
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            const float top = fmaxf(lm[n][e], mx + base[e]);
+            if (top > lm[n][e]) l[n][e] = times(l[n][e], pow2_of(lm[n][e] - top));
+            lm[n][e] = top;
+            const float from = base[e] == 0.0f ? top : mx - ((mx + base[e]) - top);
+            const float less = top == -INFINITY ? 0.0f : from;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int mk = q >> 1, at = 2 * (q & 1) + e;
+              if (kWhole || !((masked >> (4 * mk + at)) & 1u))
+                l[n][e] += ex2(fmaf(s[mk][n][at], mk == 0 ? f0[e] : f1[e], -less));
+            }
+          }
         }
         float b0[2], b1[2];
 #pragma unroll
@@ -505,7 +539,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
             p[e] = ex2(fmaf(s[mk][n][e], mk == 0 ? f0[e & 1] : f1[e & 1], mk == 0 ? b0[e & 1] : b1[e & 1]));
             if (!kWhole && ((masked >> (4 * mk + e)) & 1u))
               p[e] = 0.0f;  // (a NaN scale is not for this row's sum either)
-            else
+            else if (!far)
               l[n][e & 1] = fmaf(p[e], hh.z, l[n][e & 1]);
           }
           if (hh.y == (float)kMinExp) {
@@ -608,7 +642,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
         l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 16);
         const int r = rw * C::kRowsPerWarp + n * 8 + 2 * t + e;
         if (g == 0) {
-          s_m[kw * kRows + r] = m[n][e];
+          s_m[kw * kRows + r] = far ? lm[n][e] : m[n][e];
           s_l[kw * kRows + r] = l[n][e];
         }
       }
@@ -622,12 +656,12 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
         float mx = s_m[r];
 #pragma unroll
         for (int k = 1; k < kKW; ++k) mx = fmaxf(mx, s_m[k * kRows + r]);
-        const float w = mx == -INFINITY ? 1.0f : exp2f(m[n][e] - mx);
+        const Pow2 w = pow2_of(mx == -INFINITY ? 0.0f : m[n][e] - mx);
         float* dst = merge + (size_t)(kw * kRows + r) * C::kPitch + 4 * g;
 #pragma unroll
         for (int dg = 0; dg < kD / 32; ++dg)
-          *reinterpret_cast<float4*>(dst + dg * 32) = make_float4(o[2 * dg][n][e] * w, o[2 * dg][n][2 + e] * w,
-                                                                  o[2 * dg + 1][n][e] * w, o[2 * dg + 1][n][2 + e] * w);
+          *reinterpret_cast<float4*>(dst + dg * 32) = make_float4(times(o[2 * dg][n][e], w), times(o[2 * dg][n][2 + e], w),
+                                                                  times(o[2 * dg + 1][n][e], w), times(o[2 * dg + 1][n][2 + e], w));
       }
     __syncthreads();
     const bool complete = kb0 == 0 && kb1 == it.key_blocks;
@@ -642,7 +676,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
       float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
       for (int k = 0; k < kKW; ++k) {
-        sum += s_l[k * kRows + r] * (mx == -INFINITY ? 1.0f : exp2f(s_m[k * kRows + r] - mx));
+        sum += times(s_l[k * kRows + r], pow2_of(mx == -INFINITY ? 0.0f : s_m[k * kRows + r] - mx));
         const float4 v = *reinterpret_cast<const float4*>(merge + (size_t)(k * kRows + r) * C::kPitch + d);
         acc.x += v.x;
         acc.y += v.y;

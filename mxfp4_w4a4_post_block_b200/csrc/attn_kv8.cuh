@@ -95,6 +95,25 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
+// Sums and outputs count from a reference, the largest of score plus V exponent ev, where ev takes part up to
+// +-kFarExp: a reference then is within kFarExp of the scores' own largest, and neither a sum nor the weights that it
+// is taken from leave fp32's range (a weight is 0 at 2^-141 of the largest: -141 + 2 * 56 = -29, below a sum's 24
+// bits).  Sums counted from exponents up to 127 lost the tokens of pages with small values beside ones with large
+// values, and all of themselves at a change of reference.
+constexpr float kFarExp = 56.0f;
+__device__ __forceinline__ float near_exponent(float ev) { return fminf(fmaxf(ev, -kFarExp), kFarExp); }
+
+// 2^e as a product of two: v * 2^e may be in fp32's range where 2^e is not.
+struct Pow2 {
+  float a, b;
+};
+__device__ __forceinline__ Pow2 pow2_of(float e) {
+  e = fmaxf(e, -250.0f);  // (also -inf)
+  const float h = floorf(0.5f * e);
+  return Pow2{ex2(h), ex2(e - h)};
+}
+__device__ __forceinline__ float times(float v, Pow2 p) { return v * p.a * p.b; }
+
 // Outputs in the partials count this (attn_kv8.cu has the weights' bias).
 constexpr float kUnbias = 1.0f / 32768.0f;
 
@@ -154,17 +173,17 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_attn_kv8_join(const AttnArg
 #pragma unroll
     for (int k = 0; k < kFlight; ++k) m_new = fmaxf(m_new, pm[k]);
     // Without any maximum there is nothing to weigh (sums of zero, or of NaN).
-    const float alpha = m_new == -INFINITY ? 1.0f : exp2f(mx - m_new);
-    sum *= alpha;
+    const Pow2 alpha = pow2_of(m_new == -INFINITY ? 0.0f : mx - m_new);
+    sum = times(sum, alpha);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) acc[i] *= alpha;
+    for (int i = 0; i < kPer; ++i) acc[i] = times(acc[i], alpha);
 #pragma unroll
     for (int k = 0; k < kFlight; ++k) {
       if (c0 + k * kJW > r1) break;
-      const float w = m_new == -INFINITY ? 1.0f : exp2f(pm[k] - m_new);
-      sum = fmaf(w, pl[k], sum);
+      const Pow2 w = pow2_of(m_new == -INFINITY ? 0.0f : pm[k] - m_new);
+      sum = fmaf(w.a * pl[k], w.b, sum);
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) acc[i] = fmaf(w, v[k][i], acc[i]);
+      for (int i = 0; i < kPer; ++i) acc[i] = fmaf(w.a * v[k][i], w.b, acc[i]);
     }
     mx = m_new;
   }
@@ -188,10 +207,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_attn_kv8_join(const AttnArg
     for (int i = 0; i < kPer; ++i) acc[i] = 0.0f;
 #pragma unroll
     for (int w = 0; w < kJW; ++w) {
-      const float weight = mx == -INFINITY ? 1.0f : exp2f(s_m[first + w] - mx);
-      sum = fmaf(weight, s_l[first + w], sum);
+      const Pow2 weight = pow2_of(mx == -INFINITY ? 0.0f : s_m[first + w] - mx);
+      sum = fmaf(weight.a * s_l[first + w], weight.b, sum);
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) acc[i] = fmaf(weight, s_acc[first + w][lane * kPer + i], acc[i]);
+      for (int i = 0; i < kPer; ++i) acc[i] = fmaf(weight.a * s_acc[first + w][lane * kPer + i], weight.b, acc[i]);
     }
   }
   const float inv = sum == 0.0f ? 0.0f : kUnbias / sum;  // a row that sees nothing: zeros

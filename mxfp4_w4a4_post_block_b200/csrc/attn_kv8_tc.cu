@@ -16,7 +16,7 @@
 //    the block's scale takes the difference to the row's reference exponent, and the fp32 accumulators can
 //    grow by 2^48 past the reference before it has to move.  A weight is off by 2^-21 of that power of two.
 // The page factors: K's multiplies the scores; V's exponent ev is added to them, w = 2^(x + ev), and the sum
-// takes w 2^-ev.
+// takes w 2^-ev, or where a page's ev is beyond kFarExp exponentials of its own.
 //
 // An instruction with few columns costs the reading of its 128 x 32 bytes of K or V (45 to 80 clocks), whatever
 // its columns: so the parts and digits are columns of their own, all of them up to 24 rows (8 instructions per
@@ -51,8 +51,8 @@ constexpr int kMeta = 8;                 // tiles whose page factors are kept
 constexpr float kWeightUnit = 32.0f;     // weights count 2^-5: 20 bits, and the digits' codes 2^-25
 constexpr float kNoRef = -3.0e38f;       // no key seen yet
 constexpr float kRise = 48.0f;           // exponent that the accumulators may grow past their reference
-constexpr float kFarExp = 48.0f;         // V exponents up to it take their sums from the weights
-constexpr float kLowExp = -48.0f;        // V exponents below it do not lower the reference
+constexpr float kMostRise = kRise + 127.0f - kFarExp;  // of a block's scale: V exponents count in full there
+constexpr float kLeastRise = -111.0f;    // what lies below has fewer digits (the lowest one's scale is 2^-127)
 
 // kLive: rows of an item; kGroups: groups of four softmax warps, which take the tiles in turn and have
 // accumulators each; kSlots: ring slots; kCtas: CTAs per SM.
@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
   float* s_l = s_nb + kWarps * kLive;                                    // [kWarps][kLive]
   float* s_fac = s_l;                                                    // [kWarps][kLive] factors of a warp's weights in its sums
   float* s_ref = s_l + kWarps * kLive;                                   // [kGroups][kLive] reference exponents
-  float* s_chg = s_ref + kGroups * kLive;                                // [kGroups][kLive] what their change multiplies by
+  float* s_chg = s_ref + kGroups * kLive;                                // [kGroups][kLive] what their change multiplies by, with s_fac
   int* s_lim = reinterpret_cast<int*>(s_chg + kGroups * kLive);          // [kLive] keys that a row sees
   uint32_t* s_nan = reinterpret_cast<uint32_t*>(s_lim + kLive);          // [kLive][4] head dims that are NaN
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOffset);
@@ -477,6 +477,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
     float* const mx_of = s_mx + group * 4 * kLive;
     float* const nb_of = s_nb + warp * kLive;
     float* const fac_of = s_fac + warp * kLive;
+    float* const also_of = s_fac + group * 4 * kLive;  // (the first warp's factors have no other use meanwhile)
     const uint32_t t_o = tmem + C::kTO + group * C::kOStride + lanes;
     int pieces = 0;
     bool bad = false;  // this warp gave up a wait; its group leaves together (ok)
@@ -692,13 +693,14 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
           for (int r = 0; r < kLive; ++r) x[r] -= nb_of[r];
           __syncwarp();
         }
-        largest(fmaxf(f.y, kLowExp), mx_of + w4 * kLive, held);
+        largest(near_exponent(f.y), mx_of + w4 * kLive, held);
 #pragma unroll
         for (int k = 0; k < kHeld; ++k) {
           weights[k] = held[k];
           held[k] += base[k];
         }
-        if (__any_sync(0xffffffffu, named && f.y < kLowExp)) largest(f.y, nb_of, weights);
+        const bool far = __any_sync(0xffffffffu, named && fabsf(f.y) > kFarExp);
+        if (far) largest(f.y, nb_of, weights);
         bool outgrown = bad;
 #pragma unroll
         for (int k = 0; k < kHeld; ++k) {
@@ -722,7 +724,11 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
                   fmaxf(fmaxf(mx_of[r], mx_of[kLive + r]), fmaxf(mx_of[2 * kLive + r], mx_of[3 * kLive + r]));
               const float ref = ref_of[r];
               next[k] = top > ref + kRise ? top : ref;
-              if (w4 == 0) chg_of[r] = ref == kNoRef || next[k] == ref ? 1.0f : ex2(ref - next[k]);
+              if (w4 == 0) {
+                const Pow2 change = pow2_of(ref == kNoRef ? 0.0f : ref - next[k]);
+                chg_of[r] = change.a;
+                also_of[r] = change.b;
+              }
             }
           }
           group_sync(bar_id);
@@ -740,13 +746,13 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
                 float o[8];
                 tmem_ld_rows(t_o + part * C::kRowsN + c, o);
 #pragma unroll
-                for (int r = 0; r < 8; ++r) o[r] *= chg_of[c + r];
+                for (int r = 0; r < 8; ++r) o[r] = o[r] * chg_of[c + r] * also_of[c + r];
                 tmem_st_8(t_o + part * C::kRowsN + c, o);
               }
             asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             tc_fence_before_sync();
 #pragma unroll
-            for (int r = 0; r < kLive; ++r) l[r] *= chg_of[r];
+            for (int r = 0; r < kLive; ++r) l[r] = l[r] * chg_of[r] * also_of[r];
           }
           group_sync(bar_id);
         }
@@ -758,8 +764,11 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
         for (int k = 0; k < kHeld; ++k) {
           const int r = lane + 32 * k;
           if (r < kLive) {
-            const float rise =
-                weights[k] > kNoRef ? fminf(fmaxf(weights[k] + base[k] - ref_of[r], -111.0f), kRise) : 0.0f;
+            float rise = weights[k] > kNoRef ? fminf(weights[k] + base[k] - ref_of[r], kMostRise) : 0.0f;
+            if (rise < kLeastRise) {
+              nb_of[r] += rise - kLeastRise;
+              rise = kLeastRise;
+            }
             mx_of[w4 * kLive + r] = base[k] - ref_of[r];
             fac_of[r] = ex2(rise - 20.0f);
             uint8_t* sf = s_sfp + buf * kSfAtom + w4;
@@ -781,8 +790,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
         __syncwarp();
         // A weight is 2^(20 - rise + ev) times what the sum takes.  V exponents far apart would leave some weights
         // below fp32's range: those sums are taken on their own.
-        float unscale = __int_as_float((127 - (int)fminf(fmaxf(f.y, -kFarExp), kFarExp)) << 23);
-        if (__any_sync(0xffffffffu, named && fabsf(f.y) > kFarExp)) {
+        float unscale = __int_as_float((127 - (int)near_exponent(f.y)) << 23);
+        if (far) {
           unscale = 0.0f;
 #pragma unroll
           for (int r = 0; r < kLive; ++r) l[r] += ex2(fmaf(x[r], fs, mx_of[w4 * kLive + r]));
@@ -883,14 +892,14 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
 #pragma unroll
         for (int k = 0; k < kGroups; ++k) {
           const float ref = s_ref[k * kLive + r];
-          const float w = ref == kNoRef ? 1.0f : ex2(ref - top);  // (a group that saw no key adds its zeros, or NaN)
+          const Pow2 w = pow2_of(ref == kNoRef ? 0.0f : ref - top);  // (a group that saw no key adds its zeros, or NaN)
           const float* lk = s_l + k * 4 * kLive + r;
-          sum = fmaf(w, lk[0] + lk[kLive] + lk[2 * kLive] + lk[3 * kLive], sum);
+          sum = fmaf(w.a * (lk[0] + lk[kLive] + lk[2 * kLive] + lk[3 * kLive]), w.b, sum);
           const float4 o = *reinterpret_cast<const float4*>(s_p + k * C::kPBytes + r * 512 + lane * 16);
-          v.x = fmaf(w, o.x, v.x);
-          v.y = fmaf(w, o.y, v.y);
-          v.z = fmaf(w, o.z, v.z);
-          v.w = fmaf(w, o.w, v.w);
+          v.x = fmaf(w.a * o.x, w.b, v.x);
+          v.y = fmaf(w.a * o.y, w.b, v.y);
+          v.z = fmaf(w.a * o.z, w.b, v.z);
+          v.w = fmaf(w.a * o.w, w.b, v.w);
         }
         const uint32_t nans = s_nan[4 * r + (lane >> 3)] >> ((lane & 7) * 4);
         if (nans & 1u) v.x = __uint_as_float(0x7FC00000u);

@@ -7,7 +7,7 @@ import torch
 
 from mxfp4_w4a4_post_block_b200 import batq as BQ
 import serving_ref as R
-from test_gpu_serving import BF, F32, ok, w4a16_case, w4a16_check, w4a16_run
+from test_gpu_serving import BF, F32, attn_check, attn_run, long_table, ok, w4a16_case, w4a16_check, w4a16_run
 
 pytestmark = pytest.mark.gpu
 
@@ -60,3 +60,112 @@ def test_w4a16_nvfp4_transforms_of_far_magnitudes(x_mag, a_mag, b_mag):
     x, A, B, codes, lin, _ = w4a16_case(3, 256, 32, "nvfp4", F32, True, 32)
     x, A, B = x * x_mag, (A * np.float32(a_mag)).astype(np.float32), (B * np.float32(b_mag)).astype(np.float32)
     w4a16_check(w4a16_run(x, A, B, codes, lin, "nvfp4", F32), x, A, B, codes, lin, "nvfp4")
+
+
+# ------------------------------------------------------------------ attention
+
+def lse_check(lse, q, cu, lens, table, kc, ks, scale, max_q, digits):
+    """lse of each row against fp64, within the row's own score error: every score is off by at most `ds`, and so is
+    the logarithm of their exponentials' sum.  ds as in serving_ref.attention; beside it the exponentials (2^-21 each),
+    fp32 additions (a lane's share of the keys and the joins), what references leave out (2^-24) and lse's own rounding."""
+    page, D = kc.shape[2:]
+    T, heads, k = q.shape[0], kc.shape[1], R.e4m3_value(kc) * R.e8m0_value(ks)[..., None, None]
+    qd = q.double().numpy().reshape(T, -1, D)
+    G, got, rows = qd.shape[1] // heads, lse.double().cpu().numpy(), 0
+    q_bits = 23 if q.dtype == BF else 11
+    for b in range(len(lens)):
+        n, L = cu[b + 1] - cu[b], min(int(lens[b]), table.shape[1] * page)
+        kk = k[table[b, :(L + page - 1) // page]].transpose(1, 0, 2, 3).reshape(heads, -1, D)[:, :L]
+        for i in range(min(n, max_q)):
+            see = L - n + i + 1
+            for h in range(qd.shape[1]):
+                qq, ke = qd[cu[b] + i, h], kk[h // G][:see]
+                s, c = ke @ qq * scale, (np.abs(ke) @ np.abs(qq) * abs(scale)).max()
+                ds = c * (2.0 ** -q_bits + (D / 8 + 8) * 2.0 ** -23)
+                if digits:
+                    top = np.repeat(np.abs(qq).reshape(-1, 32).max(1), 32)
+                    eq = top * 2.0 ** -21 if q_bits > 11 else np.abs(qq) * 2.0 ** -12 + top * 2.0 ** -25
+                    ds = (np.abs(ke) @ eq).max() * abs(scale) + c * (D / 8 + 8) * 2.0 ** -23
+                ds += np.abs(s).max() * 2.0 ** -22 + 2.0 ** -15
+                want = s.max() + np.log(np.exp(s - s.max()).sum())
+                tol = ds + 2.0 ** -21 + 2.0 ** -24 + (see / 32 + 16) * 2.0 ** -23 + abs(want) * 2.0 ** -22
+                assert abs(got[cu[b] + i, h] - want) <= tol, (b, i, h, got[cu[b] + i, h], want, tol)
+                rows += 1
+    assert rows
+
+
+def spread_case(seed, kv, G, D, page, lens, scales, q_dtype=BF):
+    """One query per sequence; V's page p of each sequence has the scale byte scales(p, pages)."""
+    rng = np.random.default_rng(seed)
+    lens = np.array(lens, np.int32)
+    need = (lens + page - 1) // page
+    ids = rng.permutation(int(need.sum())).astype(np.int32)
+    table = np.full((len(lens), int(need.max())), -1, np.int32)
+    kc, ks = R.cache(rng, len(ids), kv, page, D, 0.0)
+    vc, vs = R.cache(rng, len(ids), kv, page, D, 0.0)
+    at = 0
+    for b, n in enumerate(need):
+        table[b, :n] = ids[at:at + n]
+        at += n
+        for p in range(n):
+            vs[table[b, p]] = scales(p, n)
+    vc[vs[:, 0] == 0] = 0  # what the writer leaves for zeros
+    q = torch.from_numpy(rng.standard_normal((len(lens), kv * G * D)).astype(np.float32)).to(q_dtype)
+    return [q, np.arange(len(lens) + 1).astype(np.int32), lens, table, kc, ks, vc, vs]
+
+
+ORDERS = {
+    "in turn": lambda lo, hi: lambda p, n: (lo, hi)[p & 1],
+    "low first": lambda lo, hi: lambda p, n: lo if 2 * p < n else hi,
+    "high first": lambda lo, hi: lambda p, n: hi if 2 * p < n else lo,
+    "one high page": lambda lo, hi: lambda p, n: hi if p == n // 2 else lo,
+    "one low page": lambda lo, hi: lambda p, n: lo if p == n // 2 else hi,
+    "steps": lambda lo, hi: lambda p, n: lo + (hi - lo) * p // max(n - 1, 1),
+}
+
+
+@pytest.mark.parametrize("order", list(ORDERS))
+@pytest.mark.parametrize("low,high", [(0, 247), (0, 127), (1, 247), (20, 172), (60, 200), (127, 247), (87, 167), (5, 9)])
+@pytest.mark.parametrize("D,G,page,tokens", [(64, 2, 16, 0), (64, 20, 64, 0), (128, 4, 16, 0), (128, 12, 32, 0),
+                                             (256, 2, 16, 0), (128, 4, 16, 2049), (128, 12, 64, 2049), (128, 20, 16, 2049),
+                                             (128, 40, 32, 2049)])
+def test_attention_page_scales_at_both_ends_beside_each_other(D, G, page, tokens, low, high, order):
+    """V pages whose scales lie up to 2^247 apart, in one tile and in different tiles, key groups and runs, every
+    sequence with a query: the tokens of the small ones count in the sums as the others do."""
+    lens = [2 * page, 2 * page - 3, 5 * page + 1, 700, 1, 1900]
+    c = long_table(spread_case(40, 1, G, D, page, lens, ORDERS[order](low, high)), page, tokens)
+    for b in (0, 2, 3, 5):  # (the single token's sequence has one page)
+        seen = c[7][c[3][b, :(lens[b] + page - 1) // page], 0]
+        assert seen.min() == low and seen.max() == high
+    out, lse = attn_run(*c, 0.05, 1, out_dtype=F32)
+    attn_check(out, None, *c, 0.05, 1)
+    lse_check(lse, *c[:6], 0.05, 1, tokens > 0)
+
+
+@pytest.mark.parametrize("low,high", [(0, 247), (1, 240), (40, 200)])
+@pytest.mark.parametrize("D,G,tokens", [(64, 2, 0), (128, 4, 0), (256, 4, 0), (128, 4, 2049), (128, 20, 2049), (128, 40, 2049)])
+def test_attention_scores_and_page_scales_apart(D, G, tokens, low, high):
+    """Scores that rise or fall by up to 60 along the sequence while V's scales change: references move both ways."""
+    page, lens = 32, [2000, 1999, 640, 641]
+    for order in ("low first", "high first", "steps"):
+        c = spread_case(41, 1, G, D, page, lens, ORDERS[order](low, high))
+        table, ks = c[3], c[5]
+        for b in range(4):
+            n = (lens[b] + page - 1) // page
+            for p in range(n):  # K's scale moves the scores' size; half of the sequences backwards
+                ks[table[b, p]] = 116 + 7 * (p if b & 1 else n - 1 - p) // n
+        c = long_table(c, page, tokens)
+        out, lse = attn_run(*c, 0.05, 1, out_dtype=F32)
+        attn_check(out, None, *c, 0.05, 1)
+        lse_check(lse, *c[:6], 0.05, 1, tokens > 0)
+
+
+@pytest.mark.parametrize("D,G,tokens", [(64, 4, 0), (128, 4, 0), (256, 4, 0), (128, 4, 2049), (128, 40, 2049)])
+@pytest.mark.parametrize("q_dtype", [BF, F32])
+def test_attention_log_sums(D, G, tokens, q_dtype):
+    """lse within its row's own error, one token to thousands."""
+    page, lens = 16, [1, 2, 17, 300, 2500 if tokens else 1500]
+    c = long_table(spread_case(42, 2, G, D, page, lens, lambda p, n: 119, q_dtype), page, tokens)
+    out, lse = attn_run(*c, D ** -0.5, 1, out_dtype=F32)
+    attn_check(out, None, *c, D ** -0.5, 1)
+    lse_check(lse, *c[:6], D ** -0.5, 1, tokens > 0)
