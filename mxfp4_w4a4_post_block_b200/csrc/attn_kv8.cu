@@ -456,9 +456,13 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
 #pragma unroll
-            for (int q = 0; q < 4; q += 2) {
-              s[0][n][q + e] = s[0][n][q + e] == -INFINITY ? -INFINITY : s[0][n][q + e] * f0[e];
-              s[1][n][q + e] = s[1][n][q + e] == -INFINITY ? -INFINITY : s[1][n][q + e] * f1[e];
+            for (int q = 0; q < 4; q += 2) {  // (one factor after the other: their product may leave fp32's range)
+#pragma unroll
+              for (int mk = 0; mk < 2; ++mk) {
+                const float f = mk == 0 ? h0.x : h1.x;
+                float& v = s[mk][n][q + e];
+                if (v != -INFINITY) v = f < 1.0f ? v * f * rf[n][e] : v * rf[n][e] * f;
+              }
             }
             float mx = fmaxf(fmaxf(s[0][n][e], s[0][n][2 + e]), fmaxf(s[1][n][e], s[1][n][2 + e]));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));

@@ -78,8 +78,8 @@ struct TcCfg {
   static constexpr int kMetaOffset = kSfOffset + (2 + 2 + kUnits) * kSfAtom;
   static constexpr int kRowOffset = kMetaOffset + kMeta * 8 * 16;
   // Per warp and row: maxima, weights' exponents, sums.  Per group and row: reference, its change.  Per row: keys
-  // that it sees, four words of NaN bits.
-  static constexpr int kBarOffset = kRowOffset + (3 * kWarps + 2 * kGroups + 5) * kLive * 4;
+  // that it sees, four words of NaN bits, the unit of its scores.
+  static constexpr int kBarOffset = kRowOffset + (3 * kWarps + 2 * kGroups + 6) * kLive * 4;
   static constexpr int kBars = 2 * kSlots + 12;
   static constexpr int kSmemBytes = kBarOffset + kBars * 8 + 16 * 4 + 1024;
   static constexpr int kQAtoms = kStacked ? 1 : 2;
@@ -189,6 +189,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
   float* s_chg = s_ref + kGroups * kLive;                                // [kGroups][kLive] what their change multiplies by, with s_fac
   int* s_lim = reinterpret_cast<int*>(s_chg + kGroups * kLive);          // [kLive] keys that a row sees
   uint32_t* s_nan = reinterpret_cast<uint32_t*>(s_lim + kLive);          // [kLive][4] head dims that are NaN
+  float* s_row = reinterpret_cast<float*>(s_nan + 4 * kLive);            // [kLive] units of the rows' scores, where they differ
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOffset);
   uint64_t* empty = full + kSlots;
   uint64_t* s_full = empty + kSlots;   // [2] scores are in TMEM
@@ -524,9 +525,9 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
 
       // Queries: row r is query r / G, head h * G + r % G.  A lane has four head dims, eight lanes a block of
       // 32 with the scale 2^e, |q| / 2^e < 256; the parts go to [part][row][128 bytes], swizzled.  The largest e
-      // of all rows is left to the scores' factor.
-      float common;
-      int qe[kMine], top_e = -126;
+      // of all rows is left to the scores' factor; where blocks lie further than 2^100 apart, each row has a unit
+      // of its own, 2^100 below its largest block where that is above 1, and the factor counts as infinite.
+      int qe[kMine], top_e = -126, low_e = 127;
 #pragma unroll
       for (int k = 0; k < kMine; ++k) {
         float top = 0.0f;
@@ -538,19 +539,33 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
 #pragma unroll
         for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         qe[k] = max((int)(__float_as_uint(top) >> 23) - 127 - 7, -126);
-        top_e = max(top_e, __reduce_max_sync(0xffffffffu, qe[k]));
+        top_e = max(top_e, qe[k]);
+        if (top > 0.0f) low_e = min(low_e, qe[k]);
       }
-      if (lane == 0) s_exp[warp] = top_e;
+      top_e = __reduce_max_sync(0xffffffffu, top_e);
+      low_e = __reduce_min_sync(0xffffffffu, low_e);
+      if (lane == 0) s_exp[warp] = top_e * 256 + low_e + 126;
       groups_sync<kAll>();
 #pragma unroll
-      for (int k = 0; k < kWarps; ++k) top_e = max(top_e, s_exp[k]);
-      common = e8m0_value((uint32_t)(top_e + 127));
+      for (int k = 0; k < kWarps; ++k) {
+        top_e = max(top_e, s_exp[k] >> 8);
+        low_e = min(low_e, (s_exp[k] & 255) - 126);
+      }
+      float scale = fabsf(a.scale_log2) * e8m0_value((uint32_t)(top_e + 127));
+      const bool wide = (top_e - low_e > 100 && scale != 0.0f) || scale == INFINITY;
+      if (wide) scale = INFINITY;
 #pragma unroll
       for (int k = 0; k < kMine; ++k) {
         const int r = warp + kWarps * k;
         float* v = qv[k];
-        // (the scores' factor stays positive; what lies 2^119 below the largest has no scale, and counts as zero)
-        const float f = qe[k] - top_e < -119 ? 0.0f : copysignf(e8m0_value((uint32_t)(127 - qe[k])), a.scale_log2);
+        int unit = top_e;
+        if (wide) {
+          unit = __reduce_max_sync(0xffffffffu, qe[k]);
+          if (unit > 0) unit -= 100;
+        }
+        if (wide && lane == 0) s_row[r] = fmaxf(fabsf(a.scale_log2) * e8m0_value((uint32_t)(unit + 127)), 1.4e-45f);
+        // (the scores' factor stays positive; what lies 2^119 below the unit has no scale, and counts as zero)
+        const float f = qe[k] - unit < -119 ? 0.0f : copysignf(e8m0_value((uint32_t)(127 - qe[k])), a.scale_log2);
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = fabsf(v[i]) <= 3.402823466e38f ? v[i] * f : __uint_as_float(0x7FC00000u);
 #pragma unroll
@@ -562,7 +577,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
             const bool third = !C::kStacked && part == 2;
             const int at = third ? r : n;
             s_sfq[(third ? kSfAtom : 0) + (at & 31) * 16 + (at >> 5) * 4 + (lane >> 3)] =
-                (uint8_t)max(qe[k] - top_e + 127 - 4 * part, 0);
+                (uint8_t)max(qe[k] - unit + 127 - 4 * part, 0);
           }
           const float2 lo = e4m3x2_values(c & 0xFFFFu), hi = e4m3x2_values(c >> 16);
           v[0] = (v[0] - lo.x) * 16.0f;
@@ -582,7 +597,6 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
 #pragma unroll
       for (int r = 0; r < kLive; ++r) l[r] = 0.0f;
       constexpr int kHeld = (kLive + 31) / 32;  // lane l has rows l and l + 32 of what is the warp's
-      const float scale = fabsf(a.scale_log2) * common;
       for (int i = kGroups == 1 ? 0 : (group ^ tile0) & 1; i < p.tiles; i += kGroups) {
         const int g = tile0 + i, buf = g & 1;
         const uint32_t bph = (g >> 1) & 1;
@@ -679,8 +693,11 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
 #pragma unroll
         for (int k = 0; k < kHeld; ++k) base[k] = 0.0f;
         if (__any_sync(0xffffffffu, fs > 0.125f)) {
+          // (factors one after the other: their product may leave fp32's range where the score does not)
+          const float by = s_meta[(g & (kMeta - 1)) * 8 + (gtid >> a.page_shift)].x;  // f.x again (registers)
+          const float before = by > 0.0f && by < 1.0f ? by : 1.0f, after = fs != fs ? fs : fmaxf(by, 1.0f);
 #pragma unroll
-          for (int r = 0; r < kLive; ++r) x[r] *= fs;
+          for (int r = 0; r < kLive; ++r) x[r] = x[r] * before * (scale == INFINITY ? s_row[r] : scale) * after;
           fs = 1.0f;
           largest(0.0f, nb_of, base);
 #pragma unroll

@@ -169,3 +169,44 @@ def test_attention_log_sums(D, G, tokens, q_dtype):
     out, lse = attn_run(*c, D ** -0.5, 1, out_dtype=F32)
     attn_check(out, None, *c, D ** -0.5, 1)
     lse_check(lse, *c[:6], D ** -0.5, 1, tokens > 0)
+
+
+@pytest.mark.parametrize("D,G,tokens", [(128, 4, 2049), (128, 12, 2049), (128, 20, 2049), (128, 40, 2049)])
+@pytest.mark.parametrize("q_dtype", [BF, F32])
+def test_attention_rows_at_both_ends_of_the_range_share_an_item(D, G, tokens, q_dtype):
+    """A head whose query has one value of 3e38 (its scores are finite) beside ordinary heads, whose softmax is their
+    own; and that head's other 32-dim blocks, where the keys have zeros under the large value."""
+    c = spread_case(43, 2, G, D, 16, [300, 65, 17, 1], lambda p, n: 119, q_dtype)
+    q = c[0].view(4, 2 * G, D)
+    for h in (0, G, 2 * G - 1):
+        q[:, h] = 0.0
+        q[:, h, 5] = 3e38
+    c = long_table(c, 16, tokens)
+    out, lse = attn_run(*c, 0.1, 1, out_dtype=F32)
+    attn_check(out, None, *c, 0.1, 1)
+    lse_check(lse, *c[:6], 0.1, 1, True)
+    c[4] = c[4].copy()
+    c[4][..., 5] = 0  # K has nothing there: the row's scores are those of its other blocks
+    q[:, 0, 64:] = torch.randn(4, D - 64).to(q_dtype)
+    out, lse = attn_run(*c, 0.1, 1, out_dtype=F32)
+    attn_check(out, None, *c, 0.1, 1)
+    lse_check(lse, *c[:6], 0.1, 1, True)
+
+
+@pytest.mark.parametrize("mag", [1e-11, 1e3])
+@pytest.mark.parametrize("D,G,tokens", [(64, 4, 0), (128, 4, 0), (256, 4, 0), (128, 4, 2049), (128, 40, 2049)])
+def test_attention_factors_beyond_the_range_of_scores_within(D, G, tokens, mag):
+    """K scales of 2^40 under queries of 3e38 where K's codes are zero, and under ordinary scores of small queries: the
+    product of the units is beyond fp32's range, no score is."""
+    c = spread_case(44, 1, G, D, 16, [100, 33, 5], lambda p, n: 119)
+    q = c[0].view(3, G, D)
+    q *= mag
+    q[:, 1] = 0.0
+    q[:, 1, 7] = 3e38
+    c[4] = c[4].copy()
+    c[4][..., 7] = 0
+    c[5] = np.full_like(c[5], 127 + 40 - 8)
+    c = long_table(c, 16, tokens)
+    out, lse = attn_run(*c, 0.1, 1, out_dtype=F32)
+    attn_check(out, None, *c, 0.1, 1)
+    lse_check(lse, *c[:6], 0.1, 1, tokens > 0)
