@@ -640,7 +640,8 @@ BATQ_API batq_status batq_linear_w4a16(const void* X, batq_dtype x_dtype, int S,
  * call brings among them.  The rows of sequence b are cu[b] .. cu[b + 1] - 1
  * of the call's T rows; cu == NULL: row b alone (T >= batch).  Rows behind
  * cu[batch] (padding) belong to no sequence.  A sequence whose range is not
- * inside [0, T] or is decreasing has no rows.
+ * inside [0, T] or is decreasing has no rows.  Rows in the ranges of two
+ * sequences are written to the cache for each, and have either's attention.
  *
  * (batq_quant_kv_cache writes the other cache format of this library: a scale
  * per token and 32 elements, with the block transform.)
@@ -660,8 +661,8 @@ BATQ_API batq_status batq_linear_w4a16(const void* X, batq_dtype x_dtype, int S,
  * ldk and ldv (16-byte multiples), 16-byte aligned.  Codes 16-byte aligned.
  * Tokens whose page is not named, or lies behind the page table, are dropped,
  * and so is a sequence with seq_lens[b] < n.  Rows of a page behind the new
- * tokens, and pages without new tokens, keep their bytes.  Two sequences of a
- * call must not write the same page.
+ * tokens, and pages without new tokens, keep their bytes.  A call must not
+ * write a page twice (for two sequences, or for one that names it twice).
  * Errors: BATQ_ERR_INVALID_ARG, BATQ_ERR_SHAPE, BATQ_ERR_ALIGNMENT,
  * BATQ_ERR_ARCH, BATQ_ERR_CUDA.
  */

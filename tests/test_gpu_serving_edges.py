@@ -7,7 +7,8 @@ import torch
 
 from mxfp4_w4a4_post_block_b200 import batq as BQ
 import serving_ref as R
-from test_gpu_serving import BF, F32, attn_check, attn_run, long_table, ok, w4a16_case, w4a16_check, w4a16_run
+from test_gpu_serving import (BF, F32, append_check, append_run, attn_check, attn_run, long_table, ok, w4a16_case,
+                              w4a16_check, w4a16_run)
 
 pytestmark = pytest.mark.gpu
 
@@ -210,3 +211,26 @@ def test_attention_factors_beyond_the_range_of_scores_within(D, G, tokens, mag):
     out, lse = attn_run(*c, 0.1, 1, out_dtype=F32)
     attn_check(out, None, *c, 0.1, 1)
     lse_check(lse, *c[:6], 0.1, 1, tokens > 0)
+
+
+# ------------------------------------------------------------------ the cache
+
+@pytest.mark.parametrize("page,D,dtype", [(16, 64, BF), (64, 128, F32)])
+@pytest.mark.parametrize("cu,n", [([0, 70, 0, 70, 0, 70, 0, 70], 70), ([0, 70, 5, 66, 66, 60, 69, 0, 70], 70),
+                                  ([0, 3, 0, 3, 0, 3, 0, 3, 0, 3, 0, 3], 3)])
+def test_append_rows_of_several_sequences(page, D, dtype, cu, n):
+    """Ranges of rows that overlap (every second one decreases and is empty): each sequence gets its rows, though they
+    touch more pages than rows or pages of rows."""
+    rng = np.random.default_rng(50)
+    heads, cu = 2, np.array(cu, np.int32)
+    B = len(cu) - 1
+    lens = np.array([max(int(cu[b + 1] - cu[b]), 0) + 15 + b for b in range(B)], np.int32)
+    each = -(-(n + 16 + B) // page) + 1
+    table = rng.permutation(B * each).reshape(B, each).astype(np.int32)
+    kc, ks = R.cache(rng, B * each, heads, page, D)
+    vc, vs = R.cache(rng, B * each, heads, page, D)
+    x = torch.from_numpy(rng.standard_normal((n, heads * D)).astype(np.float32)).to(dtype)
+    g = append_run(x.cuda(), x.cuda(), cu, lens, table, kc, ks, vc, vs)
+    xs = x.double().numpy().reshape(n, heads, D)
+    append_check(xs, cu, lens, table, page, kc, ks, g[0], g[1])
+    append_check(xs, cu, lens, table, page, vc, vs, g[2], g[3])
