@@ -127,6 +127,20 @@ struct HostFloats {
   }
 };
 
+// Without the interpreter's lock: a launch may wait (for a full queue, for its module to load), and a host function
+// queued ahead of it may need the lock.
+class Unlocked {
+  PyThreadState* const state_ = PyEval_SaveThread();
+
+ public:
+  ~Unlocked() { PyEval_RestoreThread(state_); }
+};
+template <class F, class... Args>
+int call(F f, Args... args) {
+  const Unlocked unlocked;
+  return f(args...);
+}
+
 int64_t mma_scale_bytes(int64_t M, int64_t columns) { return (M + 127) / 128 * 128 * ((columns + 3) / 4 * 4); }
 
 // The arrays of a ragged batch.
@@ -194,11 +208,11 @@ int linear_w4a16(PyObject* const* a) {
   if (o.rows != x.rows) refuse("out must have a row for each row of X");
   HostFloats A;
   if (a[1] != Py_None && !A.get(a[1], 64)) return kConvert;
-  return batq_linear_w4a16(x.p, x.type, x.rows, size32(N, "N"), x.ld, A.held ? A.data() : nullptr,
-                           c.floats(a[2], "B", N / 32 * 16, true), static_cast<batq_w4_format>(format),
-                           c.bytes(a[3], "w_codes", (int64_t)M * N / 2),
-                           c.bytes(a[4], "w_scales", mma_scale_bytes(M, N / (format == BATQ_W4_NVFP4 ? 16 : 32))),
-                           c.floats(a[7], "w_gs", 1, true), M, o.type, o.p, o.ld, c.stream);
+  return call(batq_linear_w4a16, x.p, x.type, x.rows, size32(N, "N"), x.ld, A.held ? A.data() : nullptr,
+              c.floats(a[2], "B", N / 32 * 16, true), static_cast<batq_w4_format>(format),
+              c.bytes(a[3], "w_codes", (int64_t)M * N / 2),
+              c.bytes(a[4], "w_scales", mma_scale_bytes(M, N / (format == BATQ_W4_NVFP4 ? 16 : 32))),
+              c.floats(a[7], "w_gs", 1, true), M, o.type, o.p, o.ld, c.stream);
 }
 
 // K, V, cu_new, seq_lens, page_table, k_codes, k_scales, v_codes, v_scales, stream
@@ -209,8 +223,8 @@ int kv8_append(PyObject* const* a) {
   const Matrix k = matrix(c, a[0], row, "K"), v = matrix(c, a[1], row, "V");
   if (k.type != v.type || k.rows != v.rows) refuse("K and V must have the same shape and type");
   const Batch b = batch(c, a[2], a[3], a[4], k.rows, "cu_new");
-  return batq_kv8_append(k.p, v.p, k.type, k.rows, m.heads, m.dim, k.ld, v.ld, b.cu, b.lens, b.table, b.count,
-                         b.max_pages, m.pages, m.page, m.k, m.ks, m.v, m.vs, c.stream);
+  return call(batq_kv8_append, k.p, v.p, k.type, k.rows, m.heads, m.dim, k.ld, v.ld, b.cu, b.lens, b.table, b.count,
+              b.max_pages, m.pages, m.page, m.k, m.ks, m.v, m.vs, c.stream);
 }
 
 // Q, cu_q, seq_lens, page_table, k_codes, k_scales, v_codes, v_scales, softmax_scale, max_q_len, workspace, out, lse, stream
@@ -229,9 +243,9 @@ int attn_kv8(PyObject* const* a) {
     const at::Tensor& l = c.tensor(a[12], "lse");
     if (l.dim() != 2 || l.size(0) != q.rows || l.size(1) != heads) refuse("lse must be T x q_heads");
   }
-  return batq_attn_kv8(q.p, q.type, q.rows, q.ld, heads, m.heads, m.dim, b.cu, b.lens, b.table, b.count, b.max_pages,
-                       m.pages, m.page, m.k, m.ks, m.v, m.vs, static_cast<float>(scale), integer(a[9], "max_q_len"),
-                       ws.first, ws.second, o.type, o.p, o.ld, c.floats(a[12], "lse", 0, true), c.stream);
+  return call(batq_attn_kv8, q.p, q.type, q.rows, q.ld, heads, m.heads, m.dim, b.cu, b.lens, b.table, b.count, b.max_pages,
+              m.pages, m.page, m.k, m.ks, m.v, m.vs, static_cast<float>(scale), integer(a[9], "max_q_len"),
+              ws.first, ws.second, o.type, o.p, o.ld, c.floats(a[12], "lse", 0, true), c.stream);
 }
 
 // a_codes, a_scales, w_codes, w_scales, expert_offsets, M, N, out, stream
@@ -240,11 +254,11 @@ int gemm_mxfp4_experts(PyObject* const* a) {
   const int M = integer(a[5], "M"), N = integer(a[6], "N");
   const int E = size32(c.tensor(a[4], "expert_offsets").numel() - 1, "experts");
   const Matrix o = matrix(c, a[7], M, "out");
-  return batq_gemm_mxfp4_experts(c.bytes(a[0], "a_codes", (int64_t)o.rows * N / 2),
-                                 c.bytes(a[1], "a_scales", (int64_t)o.rows * (N / 32)),
-                                 c.bytes(a[2], "w_codes", (int64_t)E * M * N / 2),
-                                 c.bytes(a[3], "w_scales", E * mma_scale_bytes(M, N / 32)),
-                                 c.ints(a[4], "expert_offsets"), E, o.rows, M, N, o.type, o.p, o.ld, c.stream);
+  return call(batq_gemm_mxfp4_experts, c.bytes(a[0], "a_codes", (int64_t)o.rows * N / 2),
+              c.bytes(a[1], "a_scales", (int64_t)o.rows * (N / 32)),
+              c.bytes(a[2], "w_codes", (int64_t)E * M * N / 2),
+              c.bytes(a[3], "w_scales", E * mma_scale_bytes(M, N / 32)),
+              c.ints(a[4], "expert_offsets"), E, o.rows, M, N, o.type, o.p, o.ld, c.stream);
 }
 
 // X, A, B, ratios, w_codes, w_scales, expert_offsets, M, workspace, out, stream
@@ -258,10 +272,10 @@ int linear_experts(PyObject* const* a) {
   HostFloats A;
   if (!A.get(a[1], 64)) return kConvert;
   const auto ws = buffer(c, a[8], "workspace");
-  return batq_linear_experts(x.p, x.type, x.rows, size32(N, "N"), x.ld, A.data(), c.floats(a[2], "B", N / 32 * 16),
-                             c.floats(a[3], "ratios", N / 32 * 2, true), c.bytes(a[4], "w_codes", (int64_t)E * M * N / 2),
-                             c.bytes(a[5], "w_scales", E * mma_scale_bytes(M, N / 32)),
-                             c.ints(a[6], "expert_offsets"), E, M, ws.first, ws.second, o.type, o.p, o.ld, c.stream);
+  return call(batq_linear_experts, x.p, x.type, x.rows, size32(N, "N"), x.ld, A.data(), c.floats(a[2], "B", N / 32 * 16),
+              c.floats(a[3], "ratios", N / 32 * 2, true), c.bytes(a[4], "w_codes", (int64_t)E * M * N / 2),
+              c.bytes(a[5], "w_scales", E * mma_scale_bytes(M, N / 32)),
+              c.ints(a[6], "expert_offsets"), E, M, ws.first, ws.second, o.type, o.p, o.ld, c.stream);
 }
 
 template <int (*kF)(PyObject* const*), int kArgs>

@@ -9,6 +9,7 @@ from mxfp4_w4a4_post_block_b200 import batq as BQ
 import serving_ref as R
 from test_gpu_serving import (BF, F32, append_check, append_run, attn_check, attn_run, long_table, ok, w4a16_case,
                               w4a16_check, w4a16_run)
+from test_gpu_serving_run import Layer
 
 pytestmark = pytest.mark.gpu
 
@@ -234,3 +235,39 @@ def test_append_rows_of_several_sequences(page, D, dtype, cu, n):
     xs = x.double().numpy().reshape(n, heads, D)
     append_check(xs, cu, lens, table, page, kc, ks, g[0], g[1])
     append_check(xs, cu, lens, table, page, vc, vs, g[2], g[3])
+
+
+# ------------------------------------------------------------------ threads
+
+def test_waiting_calls_let_other_threads_run():
+    """Calls that wait for a place in a full launch queue do not hold the interpreter's lock meanwhile."""
+    import threading
+    import time
+    m = Layer(60, 64, 16, 4, [3, 9])
+    b, d = m.buffers(), m.d
+    m.step(b)
+    torch.cuda.synchronize()
+    gaps, done = [0.0], threading.Event()
+
+    def tick():
+        last = time.perf_counter()
+        while not done.is_set():
+            time.sleep(0.001)
+            now = time.perf_counter()
+            gaps[0] = max(gaps[0], now - last)
+            last = now
+
+    t = threading.Thread(target=tick)
+    t.start()
+    torch.cuda._sleep(int(2e9))  # about a second, behind which the calls queue up
+    t0, longest = time.perf_counter(), 0.0
+    for _ in range(4000):
+        t1 = time.perf_counter()
+        BQ.batq_linear_w4a16(b["x"], None, None, d["w_qkv"], d["s_qkv"], b["qkv"].shape[1], b["qkv"])
+        longest = max(longest, time.perf_counter() - t1)
+    done.set()
+    t.join()
+    torch.cuda.synchronize()
+    ok()
+    assert longest > 0.3, "no call waited"
+    assert gaps[0] < 0.1, (gaps[0], longest, time.perf_counter() - t0)
