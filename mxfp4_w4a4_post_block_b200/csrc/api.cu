@@ -1,6 +1,7 @@
 // extern "C" boundary of libbatq: argument checks, host-side preparation and launches.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -21,7 +22,7 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 // Current device must be sm_100 (B200 class).  Cached per device.
 batq_status check_arch() {
-  static int state[kMaxDevices] = {0};  // 0 unknown, 1 ok, 2 bad
+  static std::atomic<int> state[kMaxDevices] = {};  // 0 unknown, 1 ok, 2 bad
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return BATQ_ERR_CUDA;
   if (dev < 0 || dev >= kMaxDevices) return BATQ_ERR_ARCH;
@@ -36,7 +37,7 @@ batq_status check_arch() {
 }
 
 unsigned* error_word() {
-  static unsigned* cached[kMaxDevices] = {nullptr};
+  static std::atomic<unsigned*> cached[kMaxDevices] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
   if (cached[dev] == nullptr) {

@@ -720,7 +720,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
 template <class C>
 cudaError_t launch_cfg(const AttnKv8Launch& L, cudaStream_t stream) {
   auto kern = k_attn_kv8<C>;
-  static int occ[64] = {0};
+  static PerDevice occ = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (occ[dev] == 0) {

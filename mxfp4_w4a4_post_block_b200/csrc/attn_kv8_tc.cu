@@ -966,13 +966,13 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
 template <class C>
 cudaError_t launch_tc(const AttnKv8Launch& L, cudaStream_t stream) {
   auto kern = k_attn_kv8_tc<C>;
-  static bool attr_set[64] = {false};
+  static PerDevice attr_set = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!attr_set[dev]) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
     if (e != cudaSuccess) return e;
-    attr_set[dev] = true;
+    attr_set[dev] = 1;
   }
   const int slots = sm_count() * C::kCtas;
   const AttnArgs a = attn_args(L, slots < kMaxRuns ? slots : kMaxRuns);

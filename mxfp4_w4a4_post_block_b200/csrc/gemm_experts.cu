@@ -530,13 +530,13 @@ cudaError_t launch_impl(const ExpertsLaunch& L, cudaStream_t stream) {
   a.ldo = L.ldo;
   a.err = L.err;
   auto kern = k_gemm_experts<kOutBF16>;
-  static bool attr_set[64] = {false};
+  static PerDevice attr_set = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!attr_set[dev]) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
-    attr_set[dev] = true;
+    attr_set[dev] = 1;
   }
   // At most one tile per expert that has rows, plus one per 256 rows, times the weight tiles.
   const long long most = ((long long)(L.E < L.T ? L.E : L.T) + L.T / kTileN) * a.tiles_m;

@@ -463,13 +463,13 @@ cudaError_t launch_cfg(const GemmLaunch* Ls, int count) {
   if (blocks >= (1LL << 31)) return cudaErrorInvalidValue;
   T.count = count;
   auto kern = k_gemm_mxfp4<BN, kSwap, kStages, kOutBF16, kFmt, kG>;
-  static bool attr_set[64] = {false};
+  static PerDevice attr_set = {};
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev >= 0 && dev < 64 && !attr_set[dev]) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
     if (e != cudaSuccess) return e;
-    attr_set[dev] = true;
+    attr_set[dev] = 1;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);

@@ -642,13 +642,13 @@ cudaError_t launch_pair_impl(const GemmLaunch* Ls, int count) {
   g.gs_w = Ls[0].gs_w;
 
   auto kern = k_gemm_pair<kOutBF16, kFmt, kG>;
-  static bool attr_set[64] = {false};
+  static PerDevice attr_set = {};
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev >= 0 && dev < 64 && !attr_set[dev]) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
     if (e != cudaSuccess) return e;
-    attr_set[dev] = true;
+    attr_set[dev] = 1;
   }
   const int clusters = g.num_units < max_clusters ? g.num_units : max_clusters;
   // Launched as a programmatic dependent of the preceding grid: set-up and

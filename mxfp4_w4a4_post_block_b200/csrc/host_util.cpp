@@ -4,7 +4,8 @@
 namespace batq {
 
 EncodeTiledFn encode_tiled_fn() {
-  static EncodeTiledFn fn = nullptr;
+  static std::atomic<EncodeTiledFn> found{nullptr};
+  EncodeTiledFn fn = found.load(std::memory_order_relaxed);
   if (fn == nullptr) {
     void* p = nullptr;
     cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
@@ -12,6 +13,7 @@ EncodeTiledFn encode_tiled_fn() {
             cudaSuccess &&
         q == cudaDriverEntryPointSuccess) {
       fn = reinterpret_cast<EncodeTiledFn>(p);
+      found.store(fn, std::memory_order_relaxed);
     }
   }
   return fn;
@@ -61,7 +63,7 @@ bool make_map_3d_swizzled(CUtensorMap* map, CUtensorMapDataType dtype, const voi
 }
 
 int sm_count() {
-  static int cached[64] = {0};
+  static PerDevice cached = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
   if (cached[dev] == 0) {

@@ -3,6 +3,7 @@
 
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cstdint>
 
 namespace batq {
@@ -27,6 +28,9 @@ bool make_map_3d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, 
 bool make_map_3d_swizzled(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, uint64_t d0, uint64_t d1,
                           uint64_t d2, uint64_t stride1_bytes, uint64_t stride2_bytes, uint32_t b0, uint32_t b1,
                           uint32_t b2, CUtensorMapSwizzle swizzle);
+
+// Values found once per device by whichever host thread comes first; 0: not yet known.
+using PerDevice = std::atomic<int>[64];
 
 // Number of SMs of the current device (cached per device).
 int sm_count();

@@ -639,13 +639,13 @@ cudaError_t launch_cfg(const LinearW4A16Launch& L, W4Args& a, cudaStream_t strea
                    kStageK / 2, kRows, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   auto kern = k_linear_w4a16<kSp, kNv, kParts>;
-  static bool attr_set[64] = {false};
+  static PerDevice attr_set = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!attr_set[dev]) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemLimit);
     if (e != cudaSuccess) return e;
-    attr_set[dev] = true;
+    attr_set[dev] = 1;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kThreads);
@@ -669,13 +669,13 @@ cudaError_t launch_cfg(const LinearW4A16Launch& L, W4Args& a, cudaStream_t strea
   // Four tokens x 4096 x 24576: 14.5 us alone, 13.1 in pairs, 14.6 in threes; one x 4096 x 4096 (32
   // tiles): 6.0 in pairs, 5.7 in fours, 6.0 in eights; one x 4096 x 18944 (one tile per SM): 10.2 alone,
   // 10.9 in pairs; 16 x 4096 x 4096: 16.3 in pairs, 11.6 in fours, 10.7 in eights.
-  static int active[64][9] = {};
+  static PerDevice active[9] = {};
   int csize = 0;
   size_t smem = 0;
   float best = 0.0f;
   for (int c = 1; c <= 8 && c <= a.stages; ++c) {
     if (!plan<kNv>(a, kSp, c, &smem)) continue;
-    if (active[dev][c] == 0) {
+    if (active[c][dev] == 0) {
       int n = sm_count();
       if (c > 1) {
         attr[1].val.clusterDim.x = (unsigned)c;
@@ -684,11 +684,11 @@ cudaError_t launch_cfg(const LinearW4A16Launch& L, W4Args& a, cudaStream_t strea
         const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
         if (e != cudaSuccess) return e;
       }
-      active[dev][c] = n < 1 ? 1 : n;
+      active[c][dev] = n < 1 ? 1 : n;
     }
-    const int full = a.tiles / active[dev][c], rest = a.tiles - full * active[dev][c];
+    const int most = active[c][dev], full = a.tiles / most, rest = a.tiles - full * most;
     float t = a.max_stages * (0.37f * full + 0.01f * a.S * kParts);
-    if (rest > 0) t += a.max_stages * std::fmax(0.1f, 0.37f * rest / active[dev][c]);
+    if (rest > 0) t += a.max_stages * std::fmax(0.1f, 0.37f * rest / most);
     if (c > 1) t += 0.6f + 0.02f * c * (full + (rest > 0 ? 1 : 0));
     if (csize == 0 || t < best) {
       csize = c;
@@ -696,7 +696,7 @@ cudaError_t launch_cfg(const LinearW4A16Launch& L, W4Args& a, cudaStream_t strea
     }
   }
   if (csize == 0 || !plan<kNv>(a, kSp, csize, &smem)) return cudaErrorInvalidConfiguration;
-  const int clusters = a.tiles < active[dev][csize] ? a.tiles : active[dev][csize];
+  const int most = active[csize][dev], clusters = a.tiles < most ? a.tiles : most;
   attr[1].val.clusterDim.x = (unsigned)csize;
   cfg.gridDim = dim3((unsigned)(clusters * csize));
   cfg.dynamicSmemBytes = smem;

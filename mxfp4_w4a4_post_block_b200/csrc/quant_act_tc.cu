@@ -391,13 +391,13 @@ cudaError_t launch_tc_impl(const QuantLaunch* Ls, const QuantArgs* as, int count
   T.count = count;
   T.num_tiles = (int)tiles;
   auto kern = k_quant_act_tc<kFmt, kNorm, kG>;
-  static bool attr_set[64] = {false};
+  static PerDevice attr_set = {};
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev >= 0 && dev < 64 && !attr_set[dev]) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
-    attr_set[dev] = true;
+    attr_set[dev] = 1;
   }
   const int grid = tiles < sm_count() ? (int)tiles : sm_count();  // one CTA per SM
   cudaLaunchConfig_t cfg = {};

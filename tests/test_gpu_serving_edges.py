@@ -271,3 +271,55 @@ def test_waiting_calls_let_other_threads_run():
     ok()
     assert longest > 0.3, "no call waited"
     assert gaps[0] < 0.1, (gaps[0], longest, time.perf_counter() - t0)
+
+
+FIRST_CALLS = """
+import sys, threading
+sys.path[:0] = [%r, %r]
+import torch
+from mxfp4_w4a4_post_block_b200 import batq as BQ
+from test_gpu_serving_run import Layer
+
+layers = [Layer(61, D, 32, 70, [900, 33, 2000, 5]) for D in (64, 128, 64, 128)]
+bufs, streams = [m.buffers() for m in layers], [torch.cuda.Stream() for _ in layers]
+torch.cuda.synchronize()
+start, errors = threading.Barrier(len(layers)), []
+
+def work(m, b, s):
+    try:
+        with torch.cuda.stream(s):
+            start.wait()
+            for _ in range(50):
+                m.step(b)
+    except Exception as e:
+        errors.append(e)
+
+threads = [threading.Thread(target=work, args=a) for a in zip(layers, bufs, streams)]
+for t in threads: t.start()
+for t in threads: t.join()
+torch.cuda.synchronize()
+assert not errors, errors
+assert BQ.batq_device_error() == 0
+want = []
+for D in (64, 128):
+    m = Layer(61, D, 32, 70, [900, 33, 2000, 5])
+    b = m.buffers()
+    m.step(b)
+    want.append(b)
+for i, b in enumerate(bufs):
+    for k in b:
+        assert torch.equal(b[k], want[i %% 2][k]), (i, k)
+print("as one thread's")
+"""
+
+
+def test_first_calls_of_several_threads():
+    """A process whose first serving calls come from four threads at once, each on its own stream (what a launcher finds
+    out at its first call is shared by all threads): results as one thread's."""
+    import os
+    import subprocess
+    import sys
+    here = os.path.dirname(os.path.abspath(__file__))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS % (os.path.dirname(here), here)], capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and "as one thread's" in r.stdout, r.stderr[-2000:]
