@@ -7,8 +7,9 @@ parallel) and linked into ``libbatq.so`` next to this file, with the CUDA
 runtime linked statically so the library loads on machines without a GPU
 driver (CUDA calls then fail with BATQ_ERR_CUDA).  binding/serving.cpp becomes
 ``_serving.so``, the Python module that marshals the serving calls' arguments
-(it uses torch's headers; the library itself does not).  Sources are only
-rebuilt when they or a header changed.
+(it uses torch's headers; the library itself does not, and is built without
+it where torch is not installed).  Sources are only rebuilt when they or a
+header changed, the module also when its command or torch did.
 """
 
 from __future__ import annotations
@@ -73,13 +74,14 @@ def _compile(src, verbose):
 
 
 def _build_serving(force):
-    """Compile the _serving module against torch's headers and libbatq.so."""
+    """Compile the _serving module against torch's headers and libbatq.so; False where there is no torch."""
     import sysconfig
 
-    import torch
-
-    if not force and not _stale(SERVING, [SERVING_SRC, os.path.join(ROOT, "include", "batq.h")]):
-        return
+    try:
+        import torch
+    except ImportError:
+        print("torch is not installed: _serving.so, which the serving calls from Python need, is not built", file=sys.stderr)
+        return False
     base = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
@@ -88,9 +90,17 @@ def _build_serving(force):
            "-I" + os.path.join(base, "include", "torch", "csrc", "api", "include"), "-I" + os.path.join(cuda, "include"),
            SERVING_SRC, "-o", SERVING, "-L" + PKG, "-l:libbatq.so", "-Wl,-rpath,$ORIGIN", "-L" + os.path.join(base, "lib"),
            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    made_by = " ".join(cmd + [torch.__version__, sys.version])
+    stamp = os.path.join(BUILD, "_serving.txt")
+    same = os.path.exists(stamp) and open(stamp).read() == made_by
+    if not force and same and not _stale(SERVING, [SERVING_SRC, os.path.join(ROOT, "include", "batq.h")]):
+        return True
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on serving.cpp:\n{r.stdout}\n{r.stderr}")
+    with open(stamp, "w") as f:
+        f.write(made_by)
+    return True
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
