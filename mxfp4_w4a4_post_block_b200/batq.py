@@ -538,7 +538,8 @@ def batq_rmsnorm_linear(X, gamma, eps, A, B, ratios, w_codes, w_scales, M, works
 # These calls run many times per generated token, and their kernels take a few microseconds, so the
 # compiled module _serving (binding/serving.cpp) reads and checks their tensors.  A tensor that is not
 # on the current device, not contiguous where it has to be, or of another shape or type raises
-# ValueError (TypeError: no tensor); other refusals raise BatqError with the library's status.
+# ValueError (TypeError: no tensor); other refusals raise BatqError with the library's status.  A call
+# without rows (X, Q, K or out of 0 x n) does nothing.
 
 _SERVING = None
 _CONVERT = -1  # _serving's answer where A is not a contiguous fp32 array

@@ -2,7 +2,8 @@
 // A decode step's kernels take 3 to 10 us, and reading the arguments' tensors from Python and passing
 // two dozen of them through ctypes took 8 to 14 us a call.  Every function takes the positional
 // arguments of the batq.py function of its name (with the stream as None or an integer), checks them,
-// calls the C ABI and returns its status; what does not fit raises ValueError or TypeError.
+// calls the C ABI and returns its status; what does not fit raises ValueError or TypeError.  A call without
+// rows (a layer whose router sent it none, a step without new tokens) has nothing to do and is not passed on.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
@@ -206,6 +207,7 @@ int linear_w4a16(PyObject* const* a) {
   const int64_t N = columns(c, a[0], "X");
   const Matrix x = matrix(c, a[0], N, "X"), o = matrix(c, a[6], M, "out");
   if (o.rows != x.rows) refuse("out must have a row for each row of X");
+  if (x.rows == 0) return BATQ_OK;
   HostFloats A;
   if (a[1] != Py_None && !A.get(a[1], 64)) return kConvert;
   return call(batq_linear_w4a16, x.p, x.type, x.rows, size32(N, "N"), x.ld, A.held ? A.data() : nullptr,
@@ -223,6 +225,7 @@ int kv8_append(PyObject* const* a) {
   const Matrix k = matrix(c, a[0], row, "K"), v = matrix(c, a[1], row, "V");
   if (k.type != v.type || k.rows != v.rows) refuse("K and V must have the same shape and type");
   const Batch b = batch(c, a[2], a[3], a[4], k.rows, "cu_new");
+  if (k.rows == 0) return BATQ_OK;
   return call(batq_kv8_append, k.p, v.p, k.type, k.rows, m.heads, m.dim, k.ld, v.ld, b.cu, b.lens, b.table, b.count,
               b.max_pages, m.pages, m.page, m.k, m.ks, m.v, m.vs, c.stream);
 }
@@ -236,6 +239,7 @@ int attn_kv8(PyObject* const* a) {
   if (o.rows != q.rows || m.dim < 1 || row % m.dim != 0) refuse("Q and out must be T x q_heads * head_dim");
   const int heads = size32(row / m.dim, "q_heads");
   const Batch b = batch(c, a[1], a[2], a[3], q.rows, "cu_q");
+  if (q.rows == 0) return BATQ_OK;
   const double scale = PyFloat_AsDouble(a[8]);
   if (scale == -1.0 && PyErr_Occurred()) throw Refused{nullptr, ""};
   const auto ws = buffer(c, a[10], "workspace");
@@ -254,6 +258,7 @@ int gemm_mxfp4_experts(PyObject* const* a) {
   const int M = integer(a[5], "M"), N = integer(a[6], "N");
   const int E = size32(c.tensor(a[4], "expert_offsets").numel() - 1, "experts");
   const Matrix o = matrix(c, a[7], M, "out");
+  if (o.rows == 0) return BATQ_OK;
   return call(batq_gemm_mxfp4_experts, c.bytes(a[0], "a_codes", (int64_t)o.rows * N / 2),
               c.bytes(a[1], "a_scales", (int64_t)o.rows * (N / 32)),
               c.bytes(a[2], "w_codes", (int64_t)E * M * N / 2),
@@ -269,6 +274,7 @@ int linear_experts(PyObject* const* a) {
   const int E = size32(c.tensor(a[6], "expert_offsets").numel() - 1, "experts");
   const Matrix x = matrix(c, a[0], N, "X"), o = matrix(c, a[9], M, "out");
   if (o.rows != x.rows) refuse("out must have a row for each row of X");
+  if (x.rows == 0) return BATQ_OK;
   HostFloats A;
   if (!A.get(a[1], 64)) return kConvert;
   const auto ws = buffer(c, a[8], "workspace");

@@ -323,3 +323,34 @@ def test_first_calls_of_several_threads():
     r = subprocess.run([sys.executable, "-c", FIRST_CALLS % (os.path.dirname(here), here)], capture_output=True, text=True,
                        timeout=300)
     assert r.returncode == 0 and "as one thread's" in r.stdout, r.stderr[-2000:]
+
+
+# ------------------------------------------------------------------ no rows
+
+def test_calls_without_rows_do_nothing():
+    """A layer without rows, a step without new tokens or sequences: nothing is written, nothing raised; what does not fit
+    is refused as with rows."""
+    m = Layer(62, 64, 16, 4, [3, 9])
+    b, d = m.buffers(), m.d
+    m.step(b)
+    kept = [t.clone() for t in d["cache"]]
+    none = torch.zeros(3, dtype=torch.int32, device="cuda")
+    q, kv, M = m.qh * 64, m.kv * 64, b["qkv"].shape[1]
+    BQ.batq_linear_w4a16(b["x"][:0], m.A, d["Bm"], d["w_qkv"], d["s_qkv"], M, b["qkv"][:0])
+    BQ.batq_linear_w4a16(torch.empty(0, m.hidden, dtype=BF, device="cuda"), None, None, d["w_qkv"], d["s_qkv"], M,
+                         torch.empty(0, M, device="cuda"))
+    BQ.batq_kv8_append(b["qkv"][:0, q:q + kv], b["qkv"][:0, q + kv:], none, b["lens"], d["table"], *d["cache"])
+    BQ.batq_kv8_append(b["qkv"][:0, q:q + kv], b["qkv"][:0, q + kv:], None, b["lens"][:0], d["table"][:0], *d["cache"])
+    BQ.batq_attn_kv8(b["qkv"][:0, :q], none, b["lens"], d["table"], *d["cache"], 0.125, 1, m.ws, b["att"][:0])
+    offsets = torch.zeros(m.E + 1, dtype=torch.int32, device="cuda")
+    BQ.batq_linear_experts(b["sorted"][:0], m.A, d["Bm"], None, d["w_e"], d["s_e"], offsets, m.M, m.ws_e, b["e"][:0])
+    codes, scales = BQ.empty_act_buffers(1, m.hidden, BQ.BATQ_SCALES_LINEAR)
+    BQ.batq_gemm_mxfp4_experts(codes[:0], scales[:0], d["w_e"], d["s_e"], offsets, m.M, m.hidden, b["e"][:0])
+    torch.cuda.synchronize()
+    ok()
+    for t, k in zip(d["cache"], kept):
+        assert torch.equal(t, k)
+    with pytest.raises(ValueError):
+        BQ.batq_linear_w4a16(b["x"][:0], m.A, d["Bm"], d["w_qkv"], d["s_qkv"], M, b["qkv"])
+    with pytest.raises(ValueError):
+        BQ.batq_attn_kv8(b["qkv"][:0, :q], None, b["lens"], d["table"], *d["cache"], 0.125, 1, m.ws, b["att"][:0])
