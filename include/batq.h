@@ -687,7 +687,8 @@ BATQ_API batq_status batq_attn_kv8_workspace_size(int max_q_len, int q_heads, in
  * Q: device, T rows of q_heads * head_dim elements (q_dtype), row stride ldq;
  * out: the same of out_dtype, row stride ldo (16-byte multiples, 16-byte
  * aligned).  max_q_len: the most queries of a sequence; queries of a longer
- * sequence behind its first max_q_len are not computed.  lse: device, T x
+ * sequence behind its first max_q_len are not computed.  (A call's time grows
+ * with it, up to T, or 1 without cu, whatever the sequences hold.)  lse: device, T x
  * q_heads fp32 or NULL: log sum_t exp(softmax_scale * <q, K_t>).
  * A query that sees no token (an empty sequence, or seq_lens[b] < n) gives
  * zeros and lse = -inf; tokens of pages that are not named are not seen;

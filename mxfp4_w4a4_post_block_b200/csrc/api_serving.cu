@@ -162,6 +162,9 @@ batq_status batq_attn_kv8(const void* Q, batq_dtype q_dtype, int T, int ldq, int
   if ((long long)batch * kv_heads * (((long long)max_q_len * (q_heads / kv_heads) + 7) / 8) >
       (1LL << 31) / (((long long)max_pages * page_size + 63) / 64 + 1))
     return BATQ_ERR_SHAPE;
+  // No sequence has more queries than there are rows, or than one without cu: what max_q_len says beyond is not paid for.
+  const int most_q = cu_q_dev ? (max_q_len < T ? max_q_len : T) : 1;
+  if ((long long)most_q * q_heads >= (1LL << 31) - 8) return BATQ_ERR_SHAPE;  // rows of the join's grid
   const long long row = (long long)q_heads * head_dim;
   st = check_rows(Q, q_dtype, row, ldq);
   if (st != BATQ_OK) return st;
@@ -192,7 +195,7 @@ batq_status batq_attn_kv8(const void* Q, batq_dtype q_dtype, int T, int ldq, int
   L.v_codes = v_codes;
   L.v_scales = v_scales;
   L.softmax_scale = softmax_scale;
-  L.max_q_len = max_q_len;
+  L.max_q_len = most_q;
   L.workspace = static_cast<float*>(workspace);
   L.out_bf16 = out_dtype == BATQ_BF16;
   L.out = out;

@@ -264,7 +264,6 @@ cudaError_t launch_join(const AttnKv8Launch& L, const AttnArgs& a, cudaStream_t 
   // No sequence can be longer than its page table: when that is one unit, no item is ever cut.
   if ((long long)L.max_pages * L.page_size <= C::kUnit) return cudaSuccess;
   const long long rows_most = (long long)L.max_q_len * a.group, rows_all = rows_most * L.kv_heads;
-  if (rows_all >= (1LL << 31) - 8) return cudaErrorInvalidConfiguration;
   // With at least a quarter as many items as runs an item has about four partials at most: a warp per row.
   const bool few = (long long)L.batch * L.kv_heads * 4 >= a.runs;
   cudaLaunchConfig_t cfg = {};

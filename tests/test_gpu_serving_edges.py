@@ -354,3 +354,33 @@ def test_calls_without_rows_do_nothing():
         BQ.batq_linear_w4a16(b["x"][:0], m.A, d["Bm"], d["w_qkv"], d["s_qkv"], M, b["qkv"])
     with pytest.raises(ValueError):
         BQ.batq_attn_kv8(b["qkv"][:0, :q], None, b["lens"], d["table"], *d["cache"], 0.125, 1, m.ws, b["att"][:0])
+
+
+@pytest.mark.parametrize("D,G,tokens", [(64, 2, 0), (128, 2, 2049), (256, 2, 0)])
+def test_attention_more_queries_allowed_than_there_are(D, G, tokens):
+    """A generous max_q_len: what a call of the most that can be (T rows; one without cu) gives, and as fast."""
+    rng = np.random.default_rng(63)
+    c = list(spread_case(63, 2, G, D, 16, [300, 1200, 41], lambda p, n: 119))
+    c[0] = torch.from_numpy(rng.standard_normal((7, 2 * G * D)).astype(np.float32)).to(BF)
+    c[1] = np.array([0, 5, 5, 7], np.int32)
+    c = long_table(c, 16, tokens)
+    for cu, most in ((c[1], 7), (None, 1)):
+        want = attn_run(c[0], cu, *c[2:], 0.1, most)
+        for m in (most + 1, 300000):
+            got = attn_run(c[0], cu, *c[2:], 0.1, m)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    # the time of a call that is told 300000 beside one that is told 1
+    d = [R.cuda(a) for a in c[2:]]
+    q, out = c[0].cuda(), torch.empty(7, 2 * G * D, dtype=BF, device="cuda")
+    ws = torch.empty(BQ.batq_attn_kv8_workspace_size(300000, 2 * G, 2, D), dtype=torch.uint8, device="cuda")
+    times = []
+    for m in (1, 300000):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        for i in range(60):
+            if i == 10:
+                a.record()
+            BQ.batq_attn_kv8(q, None, *d, 0.1, m, ws, out)
+        b.record()
+        torch.cuda.synchronize()
+        times.append(a.elapsed_time(b))
+    assert times[1] < 2 * times[0] + 0.2, times

@@ -203,3 +203,13 @@ def test_reference_append_grows_scales():
     step = np.exp2(np.array([exps[1, 0]] * 16 + [exps[0, 0]] * 4) - 9.0)[:, None]
     # half a step of 2^-3 relative, twice for codes that were rounded again, and half of the smallest step
     assert (np.abs(got - x[:, 0]) <= np.abs(x[:, 0]) * 2.0 ** -3 + step).all()
+
+
+def test_attn_kv8_refuses_more_rows_than_a_grid_has(L):
+    """Rows of the join's grid stay below 2^31 - 8, and are refused before anything is launched."""
+    #       Q    type T          ldq qh heads dim cu   lens  table B max_pages pages page kc    ks    vc    vs   scale max_q
+    args = [FAKE, 1, (1 << 31) - 1, 64, 1, 1, 64, FAKE, FAKE, FAKE, 1, 1, 20, 128, FAKE, FAKE, FAKE, FAKE, 0.125,
+            (1 << 31) - 8, FAKE, 1 << 30, 1, FAKE, 64, None, None]
+    assert L.batq_attn_kv8(*args) == SHAPE
+    args[19], args[0] = (1 << 31) - 9, FAKE + 2  # as far as the next refusal
+    assert L.batq_attn_kv8(*args) == ALIGN
