@@ -650,7 +650,13 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
           s_l[kw * kRows + r] = l[n][e];
         }
       }
-    __syncthreads();  // every tile has been read: the ring's memory is free
+    // Every tile has been read: the ring's memory is free.  Where a warp gave up a wait the CTA ends, once its copies
+    // have landed.
+    if (__syncthreads_or(!ok)) {
+      if (rw == 0)
+        for (int i = 0; i < kSlots; ++i) mbar_wait_warp(&full[i], i < p_slot ? p_phase : p_phase ^ 1);
+      return;
+    }
     float* merge = reinterpret_cast<float*>(smem);
 #pragma unroll
     for (int n = 0; n < kNT; ++n)

@@ -152,7 +152,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint64_t* sf_ready = acc_empty + 1;  // [kStages], leader only
   uint64_t* sx_full = sf_ready + kStages;  // [kSxSlots], leader only
   uint64_t* sx_empty = sx_full + kSxSlots;
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sx_empty + kSxSlots);
+  uint64_t* all_done = sx_empty + kSxSlots;  // products and scale copies have ended, leader only
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(all_done + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -174,6 +175,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     mbar_init(acc_full, 1);
     mbar_init(acc_empty, 2 * kEpiWarps);
+    mbar_init(all_done, 2);
     fence_barrier_init();
     griddep_launch_dependents();
   }
@@ -369,6 +371,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
       }
+      // All instructions have ended before TMEM is freed, given up or not.
+      if (issuer) tc_commit_pair_local(all_done);
+      __syncwarp();
+      if (!mbar_wait_warp(all_done, 0) && issuer) set_error(a.err, kErrMmaTimeout);
+      // Where any role gave up this one does too, and copies may be on their way (of both CTAs, on the leader's barriers):
+      // each stage's barrier gets its time, in the phase that it is in.
+      for (int i = 0; !ok && i < 2 * kStages; ++i) mbar_wait_warp(&full[i >> 1], i & 1);
     }
   } else if (warp == kSfWarp) {
     // ---------------------- scale copies into TMEM (leader only) ----------------------
@@ -412,6 +421,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
       }
+      if (issuer) tc_commit_pair_local(all_done);
+      __syncwarp();
     }
   } else {
     // ------------------------------ epilogue (both CTAs) ------------------------------

@@ -222,7 +222,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* acc_full = empty + kMaxRing;
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* sums_ready = acc_empty + 2;
-  uint64_t* made = sums_ready + 2;                                         // [kMaxPasses] digits of a pass
+  uint64_t* all_done = sums_ready + 2;                                     // products have ended
+  uint64_t* made = all_done + 1;                                           // [kMaxPasses] digits of a pass
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(made + kMaxPasses);
 
   uint32_t csize, crank;
@@ -239,6 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
+    mbar_init(all_done, 1);
     for (int i = 0; i < kMaxPasses; ++i) mbar_init(&made[i], kMakerWarps);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
@@ -283,6 +285,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             ph ^= 1;
           }
         }
+      // Every copy has landed before the CTA may end, given up or not.
+      for (int i = 0; i < a.ring; ++i)
+        if (!mbar_wait(&full[i], i < s ? ph : ph ^ 1)) set_error(a.err, kErrDataTimeout);
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------ scale copies and MMAs ------------------------------
@@ -365,6 +370,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+    // All instructions have ended before TMEM is freed, given up or not.
+    tc_commit(all_done);
+    if (!mbar_wait(all_done, 0)) set_error(a.err, kErrMmaTimeout);
     }
   } else {
     // ------------------------------ digits ------------------------------
@@ -621,7 +629,7 @@ bool plan(W4Args& a, int sp, int csize, size_t* smem) {
   a.max_stages = (a.stages + csize - 1) / csize;
   a.n = (a.parts * sp + 15) & ~15;
   const size_t fixed = (size_t)a.max_stages * (a.n * 128 + kAtoms * kSfAtom) + 2 * (size_t)(kRows + 8) * sp * 4 + 32 * 4 +
-                       (2 * kMaxRing + 6 + kMaxPasses) * 8 + 16 + 1024;
+                       (2 * kMaxRing + 7 + kMaxPasses) * 8 + 16 + 1024;
   a.acc_stride = (a.n + 31) & ~31;
   a.t_sx = 2 * a.acc_stride;
   a.t_sw = a.t_sx + a.max_stages * 4 * kAtoms;
