@@ -285,9 +285,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             ph ^= 1;
           }
         }
-      // Every copy has landed before the CTA may end, given up or not.
-      for (int i = 0; i < a.ring; ++i)
-        if (!mbar_wait(&full[i], i < s ? ph : ph ^ 1)) set_error(a.err, kErrDataTimeout);
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------ scale copies and MMAs ------------------------------
@@ -312,6 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int buf = it & 1;
       if (!mbar_wait(&acc_empty[buf], ((it >> 1) & 1) ^ 1)) {
         set_error(a.err, kErrDrainTimeout);
+        ok = false;
         break;
       }
       tc_fence_after_sync();
@@ -373,6 +371,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // All instructions have ended before TMEM is freed, given up or not.
     tc_commit(all_done);
     if (!mbar_wait(all_done, 0)) set_error(a.err, kErrMmaTimeout);
+    // Where any role gave up this one does too, and copies may be on their way: each slot's barrier gets its time, in
+    // the phase that it is in.  (Waiting for all slots always took 0.5 us of 3.4 for one token x 512 x 512.)
+    for (int i = 0; !ok && i < 2 * a.ring; ++i) mbar_wait(&full[i >> 1], i & 1);
     }
   } else {
     // ------------------------------ digits ------------------------------
