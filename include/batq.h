@@ -615,9 +615,11 @@ typedef enum { BATQ_W4_MXFP4 = 0, BATQ_W4_NVFP4 = 1 } batq_w4_format;
  * A_host, B_dev: as batq_quant_act, or both NULL.
  * w_codes, w_scales: M rows, MMA scale layout.  w_gs_dev: NVFP4 only, the
  *    device float that batq_prepare_weights_nvfp4 wrote, or NULL (1).
- * Accuracy: y is rounded to 2^-13 (bf16 out) or 2^-22 (fp32 out) of the power
- * of two at or below the largest of its 32 neighbours (NVFP4: 16, and to 2^-25
- * or 2^-34 of the token's largest); products are exact and summed in fp32.
+ * Accuracy: y is rounded to 2^-16 (bf16 out) or 2^-22 (fp32 out) of the power
+ * of two at or below the largest of its 32 neighbours (NVFP4: of 16, and to
+ * 2^-33 or 2^-39 of a bound on the token's values: the largest of 4 |x| |B_i|
+ * times the largest column sum of |A|, of |x| without a transform); products
+ * are exact and summed in fp32.
  * A non-finite x makes all outputs of its token NaN.
  * Errors: BATQ_ERR_INVALID_ARG (also: only one of A_host and B_dev, w_gs_dev
  * with MXFP4), BATQ_ERR_SHAPE (S > 16, N % 64 != 0, N > 98304 or

@@ -11,10 +11,12 @@
 // and written in radix 8 with the digits -4 .. 3, which are E2M1 values,
 //   y = 2^e (d_0 + d_1 / 8 + d_2 / 64 + ..),   |y| < 2 * 2^e,
 // one column of the N side per token and digit, all digits of a block under the block's scale, and
-// the digits' accumulators are added with the weights 1, 1/8, 1/64, .. in the epilogue.  Five digits
-// (2^-13 of the block's largest value) serve a bf16 output, eight (2^-22) an fp32 one; sixteen tokens
-// then are 80 or 128 of the 256 columns an instruction can have, and the tensor pipe still waits for
-// memory.  (With the weights widened to f16 in registers for m16n8k16 instructions, the same products
+// the digits' accumulators are added with the weights 1, 1/8, 1/64, .. in the epilogue.  Six digits
+// (2^-16 of the block's largest value, so that a value 2^7 below it still has bf16's bits) serve a bf16
+// output, eight (2^-22) an fp32 one; sixteen tokens then are 96 or 128 of the 256 columns an instruction
+// can have, and the tensor pipe still waits for memory.  (Five digits are as fast up to four tokens and 2
+// to 4 % faster for sixteen, 11.0 instead of 11.5 us for 16 x 4096 x 4096, but lose bits of bf16 tokens
+// beside values 2^4 larger, as outlier channels are.  With the weights widened to f16 in registers for m16n8k16 instructions, the same products
 // were bound by the conversions: 4 tokens x 4096 x 24576 took 30 us, 16 tokens 113 us.)
 //
 // A CTA makes its tokens' digits once, keeps them and their scales (shared memory, TMEM), and walks
@@ -54,7 +56,7 @@ constexpr int kStageBytes = kRows * kStageK / 2;
 constexpr int kSfAtom = 512;
 constexpr int kMaxRing = 10;
 constexpr int kMaxPasses = 32;                   // of the makers over their items (the digits' space allows 14)
-constexpr int kPartsBf16 = 5, kPartsF32 = 8;     // digits by output type
+constexpr int kPartsBf16 = 6, kPartsF32 = 8;     // digits by output type
 
 struct W4Args {
   const void* X;
@@ -488,8 +490,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         v[i] = __float_as_uint(fmaf(y[i] * inv, kUnit, 12582912.0f)) + (kFours - 0x4B400000u);
-      // Two numbers to a register: the last five digits (15 bits), and of eight the first four.
-      constexpr int kLow = kParts == 5 ? 5 : 4;
+      // Two numbers to a register: of six digits the last five (15 bits) and the first, of eight four each.
+      constexpr int kLow = kParts == 8 ? 4 : 5;
       uint32_t low[4], high[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {

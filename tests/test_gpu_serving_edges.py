@@ -384,3 +384,26 @@ def test_attention_more_queries_allowed_than_there_are(D, G, tokens):
         torch.cuda.synchronize()
         times.append(a.elapsed_time(b))
     assert times[1] < 2 * times[0] + 0.2, times
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("S", [1, 3, 8, 16])
+@pytest.mark.parametrize("x_dtype", [BF, F32])
+def test_w4a16_bf16_outputs_beside_an_outlier(S, x_dtype, fmt):
+    """A value 2^11 above its block's others, whose weights are zero: the outputs come of the others alone, which are
+    kept to 2^-16 of it (and the output to 2^-8 of itself)."""
+    N, M, rng = 64, 1040, np.random.default_rng(33)
+    codes, lin = R.random_weights(rng, M, N, fmt)
+    codes[:, 10 // 2] &= 0xF0  # element 10's codes (the low nibble) are +0
+    x = torch.from_numpy(rng.uniform(-1, 1, (S, N)).astype(np.float32)).to(x_dtype)
+    x[:, 10] = 2047.0 if x_dtype == F32 else 2040.0  # (below 2^11: the block's power of two is 2^10)
+    out = w4a16_run(x, None, None, codes, lin, fmt, BF)
+    w, xd = R.weights(codes, lin, fmt), x.double().numpy()
+    ref = xd @ w.T
+    G = 32 if fmt == "mxfp4" else 16
+    each = np.where(np.arange(N) // G == 10 // G, 2.0 ** -16 * 2.0 ** 10, 2.0 ** -16)
+    if fmt == "nvfp4":
+        each = each + 2.0 ** -33 * 2.0 ** 11
+    tol = each @ np.abs(w).T + (np.abs(xd) * (np.arange(N) != 10)) @ np.abs(w).T * (N / 8 + 24) * 2.0 ** -23 + np.abs(ref) * 2.0 ** -8
+    err = np.abs(out.double().cpu().numpy() - ref)
+    assert (err <= tol).all(), (err / tol).max()
