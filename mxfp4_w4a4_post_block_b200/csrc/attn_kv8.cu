@@ -31,8 +31,8 @@
 // What bounds it is the issue of instructions: widening K and V, the softmax's and the loads' address
 // arithmetic are about 820 of them per 32 keys and 8 rows, at half of the issue slots; so head dim 128 with
 // long page tables has the kernel in attn_kv8_tc.cu.  Measured: 16 sequences of up to 16000 tokens, 4 heads of
-// 8 queries: 31 us at head dim 64 (3.6 TB/s), 64 us at 256 (4.6 TB/s); 3 sequences of 100 tokens 6 us, the
-// launch and one tile's way through it.  More rows cost more softmax: five queries each 70 and 123 us.
+// 8 queries: 33 us at head dim 64 (2.1 TB/s), 67 us at 256 (4.2 TB/s); 3 sequences of 100 tokens 6 us, the
+// launch and one tile's way through it.  More rows cost more softmax: five queries each 75 and 127 us.
 #include <cstdint>
 #include <type_traits>
 
@@ -97,10 +97,14 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 // bias puts that one at 2^15, and f16's smallest step 2^39 below it) however far apart the blocks'
 // scales are, and the accumulators need no unit of their own.  Scales below 2^kMinExp (an all-zero
 // block has 2^-127) ride as 2^kMinExp, and the rest multiplies the f16 weights.  From the first tile
-// on whose |ev| is beyond kFarExp, a sum has a reference of its own (kFarExp has which) and
-// exponentials of its own; a piece's outputs are brought to that reference at its end.
+// on whose |ev| is beyond kSameExp, a sum has a reference of its own (kFarExp has which) and
+// exponentials of its own; a piece's outputs are brought to that reference at its end.  (Up to there
+// the factor 2^(m - m') of a new maximum leaves fp32's range only where the sum so far has no bits in
+// the new one: -126 + 2 * 48 = -30.)
 constexpr int kBias = 15;
 constexpr int kMinExp = -100;
+constexpr float kSameExp = 48.0f;
+static_assert(kSameExp <= kFarExp, "the reference so far is the sum's own");
 __device__ __forceinline__ float v_exponent(int byte) {
   return byte == 255 ? __uint_as_float(0x7FC00000u) : (float)max(byte - 127, kMinExp);
 }
@@ -113,6 +117,38 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
+}
+
+// Adds the exponentials of a tile's scores to two rows' sums whose references stand at `ref` and `ref + 1`: a, b the
+// scores of the halves' keys as they lie (row 0, row 1, row 0, row 1), f their factors (a's two, b's two), e_base V's
+// exponents and what the scores count from, bit 4 b + i of `masked` a score that is not.  (A call, since its code in
+// the tiles' own cost them 2 to 6 % of their time.)
+__device__ __noinline__ float2 far_sums(const float4 a, const float4 b, const float4 f, const float4 e_base, const float2 l,
+                                        const uint32_t masked, float* const ref) {
+  const float s[2][4] = {{a.x, a.y, a.z, a.w}, {b.x, b.y, b.z, b.w}};
+  const float fs[2][2] = {{f.x, f.y}, {f.z, f.w}}, base[2] = {e_base.z, e_base.w};
+  float sums[2] = {l.x, l.y};
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    float mx = fmaxf(fmaf(fmaxf(s[0][e], s[0][2 + e]), fs[0][e], near_exponent(e_base.x)),
+                     fmaf(fmaxf(s[1][e], s[1][2 + e]), fs[1][e], near_exponent(e_base.y)));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+    const float before = ref[e], top = fmaxf(before, mx + base[e]);
+    if (top > before) sums[e] = times(sums[e], pow2_of(before - top));
+    __syncwarp();
+    if ((threadIdx.x & 28) == 0) ref[e] = top;
+    __syncwarp();
+    const float from = base[e] == 0.0f ? top : mx - ((mx + base[e]) - top);
+    const float less = top == -INFINITY ? 0.0f : from;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int mk = q >> 1, at = 2 * (q & 1) + e;
+      if (!((masked >> (4 * mk + at)) & 1u)) sums[e] += ex2(fmaf(s[mk][at], fs[mk][e], -less));
+    }
+  }
+  return make_float2(sums[0], sums[1]);
 }
 
 template <class C>
@@ -346,8 +382,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
     // This lane's rows: 8 n + 2 t and the next of its warp's; keys of a tile: 16 mk + g and + 8.
     float o[kD / 16][kNT][4];
     float m[kNT][2], l[kNT][2], rf[kNT][2];
-    float lm[kNT][2];  // the sums' reference, where it is not m
-    bool far = false;  // it is not (the same for the warp)
+    bool far = false;  // the sums' references are not m (the same for the warp), and stand in s_m
     int lim[kNT][2];
 #pragma unroll
     for (int n = 0; n < kNT; ++n) {
@@ -356,7 +391,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int r = rw * C::kRowsPerWarp + n * 8 + 2 * t + i;
-        m[n][i] = lm[n][i] = -INFINITY;
+        m[n][i] = -INFINITY;
         l[n][i] = 0.0f;
         rf[n][i] = s_rf[r];
         lim[n][i] = min(lim0 + (rt * kRows + r) / a.group, it.s.len);
@@ -381,7 +416,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
       return ok = false;
     };
     // Tile i, whose K has landed.  kWhole: nothing of it is masked (all but a sequence's last tiles).
-    auto tile = [&](auto whole_tag, const int i, const int key, const float4 h0, const float4 h1) {
+    auto tile = [&](auto whole_tag, const int i, const int key, float4 h0, float4 h1) {
       constexpr bool kWhole = decltype(whole_tag)::value;
       const uint32_t named = kWhole ? 3u : __float_as_uint(h0.w);
 
@@ -419,14 +454,16 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
         }
       }
       release(2 * i);
-      if (!far && fmaxf(fabsf(h0.y), fabsf(h1.y)) > kFarExp) {
+      if (!far && fmaxf(fabsf(h0.y), fabsf(h1.y)) > kSameExp) {
         far = true;
+        if (g == 0)
 #pragma unroll
-        for (int n = 0; n < kNT; ++n) {
-          lm[n][0] = m[n][0];
-          lm[n][1] = m[n][1];
-        }
+          for (int n = 0; n < kNT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) s_m[kw * kRows + rw * C::kRowsPerWarp + n * 8 + 2 * t + e] = m[n][e];
+        __syncwarp();
       }
+      if (far) h0.z = h1.z = 0.0f;  // what sums take of the weights
 
       // Softmax.  The maximum is taken of the raw scores, whose factor is positive.
       uint32_t pb[2][kNT][2];  // P^T: the second product's operand
@@ -493,10 +530,9 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
           float alpha[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const Pow2 change = pow2_of(m_new[e] > m[n][e] ? m[n][e] - m_new[e] : 0.0f);
-            alpha[e] = change.a * change.b;  // (outputs below 2^-126 of the largest product are beyond f16's steps)
+            alpha[e] = m_new[e] > m[n][e] ? ex2(m[n][e] - m_new[e]) : 1.0f;
             m[n][e] = m_new[e];
-            if (!far) l[n][e] = times(l[n][e], change);
+            if (!far) l[n][e] *= alpha[e];
           }
 #pragma unroll
           for (int d = 0; d < kD / 16; ++d)
@@ -504,26 +540,13 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
             for (int e = 0; e < 4; ++e) o[d][n][e] *= alpha[e & 1];
         }
         if (far) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float x0 = fmaf(fmaxf(s[0][n][e], s[0][n][2 + e]), f0[e], near_exponent(h0.y));
-            const float x1 = fmaf(fmaxf(s[1][n][e], s[1][n][2 + e]), f1[e], near_exponent(h1.y));
-            float mx = fmaxf(x0, x1);
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            const float top = fmaxf(lm[n][e], mx + base[e]);
-            if (top > lm[n][e]) l[n][e] = times(l[n][e], pow2_of(lm[n][e] - top));
-            lm[n][e] = top;
-            const float from = base[e] == 0.0f ? top : mx - ((mx + base[e]) - top);
-            const float less = top == -INFINITY ? 0.0f : from;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const int mk = q >> 1, at = 2 * (q & 1) + e;
-              if (kWhole || !((masked >> (4 * mk + at)) & 1u))
-                l[n][e] += ex2(fmaf(s[mk][n][at], mk == 0 ? f0[e] : f1[e], -less));
-            }
-          }
+          const float2 sums =
+              far_sums(make_float4(s[0][n][0], s[0][n][1], s[0][n][2], s[0][n][3]),
+                       make_float4(s[1][n][0], s[1][n][1], s[1][n][2], s[1][n][3]), make_float4(f0[0], f0[1], f1[0], f1[1]),
+                       make_float4(h0.y, h1.y, base[0], base[1]), make_float2(l[n][0], l[n][1]), masked,
+                       s_m + kw * kRows + rw * C::kRowsPerWarp + n * 8 + 2 * t);
+          l[n][0] = sums.x;
+          l[n][1] = sums.y;
         }
         float b0[2], b1[2];
 #pragma unroll
@@ -543,7 +566,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
             p[e] = ex2(fmaf(s[mk][n][e], mk == 0 ? f0[e & 1] : f1[e & 1], mk == 0 ? b0[e & 1] : b1[e & 1]));
             if (!kWhole && ((masked >> (4 * mk + e)) & 1u))
               p[e] = 0.0f;  // (a NaN scale is not for this row's sum either)
-            else if (!far)
+            else
               l[n][e & 1] = fmaf(p[e], hh.z, l[n][e & 1]);
           }
           if (hh.y == (float)kMinExp) {
@@ -646,7 +669,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
         l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 16);
         const int r = rw * C::kRowsPerWarp + n * 8 + 2 * t + e;
         if (g == 0) {
-          s_m[kw * kRows + r] = far ? lm[n][e] : m[n][e];
+          if (!far) s_m[kw * kRows + r] = m[n][e];
           s_l[kw * kRows + r] = l[n][e];
         }
       }
@@ -666,12 +689,12 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
         float mx = s_m[r];
 #pragma unroll
         for (int k = 1; k < kKW; ++k) mx = fmaxf(mx, s_m[k * kRows + r]);
-        const Pow2 w = pow2_of(mx == -INFINITY ? 0.0f : m[n][e] - mx);
+        const float w = mx == -INFINITY ? 1.0f : exp2f(m[n][e] - mx);
         float* dst = merge + (size_t)(kw * kRows + r) * C::kPitch + 4 * g;
 #pragma unroll
         for (int dg = 0; dg < kD / 32; ++dg)
-          *reinterpret_cast<float4*>(dst + dg * 32) = make_float4(times(o[2 * dg][n][e], w), times(o[2 * dg][n][2 + e], w),
-                                                                  times(o[2 * dg + 1][n][e], w), times(o[2 * dg + 1][n][2 + e], w));
+          *reinterpret_cast<float4*>(dst + dg * 32) = make_float4(o[2 * dg][n][e] * w, o[2 * dg][n][2 + e] * w,
+                                                                  o[2 * dg + 1][n][e] * w, o[2 * dg + 1][n][2 + e] * w);
       }
     __syncthreads();
     const bool complete = kb0 == 0 && kb1 == it.key_blocks;
