@@ -707,9 +707,11 @@ BATQ_API batq_status batq_attn_kv8_workspace_size(int max_q_len, int q_heads, in
  * fp32 queries keep 12 bits, and those products are rounded to 2^-20 of the
  * largest among their 32 tokens (2^-60 of the row's largest).  The scales of a
  * row's pages may lie anywhere in E8M0's range; a token whose probability is
- * below 2^-126 of the row's largest may count as none.  The split of the work depends only on the
- * lengths, so results repeat bit for bit.  Non-finite queries, and scores
- * beyond fp32's range, give NaN.
+ * below 2^-126 of the row's largest may count as none.  The split of the work
+ * depends on the lengths, on max_q_len (up to T) and, for head dim 128, on
+ * which of the two forms the page table's width gives, so a call repeats bit
+ * for bit, and the same request in a wider table need not.  Non-finite
+ * queries, and scores beyond fp32's range, give NaN.
  * workspace: device, 16-byte aligned; calls that may overlap need one each.
  * Errors: BATQ_ERR_INVALID_ARG (softmax_scale not finite), BATQ_ERR_SHAPE,
  * BATQ_ERR_ALIGNMENT, BATQ_ERR_WORKSPACE, BATQ_ERR_ARCH, BATQ_ERR_CUDA.

@@ -33,8 +33,8 @@
 // 16000 tokens with 40 rows).  The work list, the runs and the join are attn_kv8.cuh's; an item counts kOver
 // units beside its keys (0 -> 4 and 12: 109 -> 100 us and 86 -> 72 us in those cases).
 //
-// Measured: 64 x up to 8192 tokens, 8 heads of 4 queries: 100 us, 5.9 TB/s; one sequence of 131072: 50 us,
-// 5.4 TB/s; both close to the memory's rate.  16 x up to 16000 tokens with 40 rows: 62 us, where the chain of
+// Measured: 64 x up to 8192 tokens, 8 heads of 4 queries: 103 us, 5.7 TB/s; one sequence of 131072: 51 us,
+// 5.3 TB/s; both close to the memory's rate.  16 x up to 16000 tokens with 40 rows: 62 us, where the chain of
 // a tile bounds it (scores, softmax of 40 rows per key, products; memory 20 us).
 #include "attn_kv8.cuh"
 

@@ -23,7 +23,8 @@
 // neighbouring lanes so that a store writes two consecutive out-features of one token (64
 // contiguous bytes per token and warp).  Rows outside every group are not written.
 //
-// Measured: 16384 rows of 8 experts, 4096 x 4096: 131 us (4.2 PFLOP/s), bound by the tensor pipe with the
+// Measured: 16384 rows of 8 experts, 4096 x 4096: 131 us (4.2 PFLOP/s) in a short row of calls, 152 to 157 us
+// (3.5 PFLOP/s) in a long one, bound by the tensor pipe with the
 // scale copies in its queue and by one accumulator; 8190 rows of 128 experts, 2112 x 1040: 47 us, 64 rows
 // of 64, 4096 x 2048: 33 us, bound by memory and by stages and tiles that are nearly empty but take as
 // long as whole ones (stages of K = 256: 57 and 42 us).

@@ -14,7 +14,7 @@
 // maximum to the codes; larger blocks are read twice, eight chunks at a time, the second time from L2.
 // (One chunk at a time, each with its own trip to memory: 23.7 us for 8000 rows of 8 x 128 instead of
 // 17.1.)  The maximum is taken of the bits as integers, two bf16 at a time, and values are checked for NaN and
-// infinities only where that maximum shows some (17.2 -> 14.7 us; memory 11.3).  One token of 64 sequences: 4.2 us,
+// infinities only where that maximum shows some (17.2 -> 15.1 us; memory 11.3).  One token of 64 sequences: 4.3 us,
 // the launch and three dependent reads.
 #include <cstdint>
 #include <type_traits>

@@ -31,7 +31,7 @@
 // What bounds it: at one tile per CTA the chain of launch, digits (1.4 us per unit of a warp), products
 // and exchange; with many the stream of weights.  Measured: one token x 4096 x 4096 5.7 us (1.5 TB/s; an
 // empty kernel's launch takes 2.5), four x 4096 x 24576 13.0 us (4.1 TB/s), seven x 12288 x 4096 NVFP4
-// with fp32 out 12.5 us (2.3 TB/s), 16 x 4096 x 24576 22 us.
+// with fp32 out 12.5 us (2.3 TB/s), 16 x 4096 x 24576 23.7 us.
 #include <cfloat>
 #include <cmath>
 #include <cstdint>
