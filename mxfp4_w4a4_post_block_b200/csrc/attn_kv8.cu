@@ -42,12 +42,15 @@ namespace batq {
 namespace {
 
 constexpr int kTile = 32;  // keys per tile
+constexpr int kBias = 15;  // of the weights' exponents (below)
+constexpr float kUnbias = 1.0f / (1 << kBias);
 
 // kD: head dim; kNT: 8-row tiles per warp; kRW: row warps; kKW: key groups; kSlots: ring slots (a K or
 // a V tile each) per key group; kCtas: CTAs per SM that registers and shared memory are laid out for.
 template <int kD_, int kNT_, int kRW_, int kKW_, int kSlots_, int kCtas_>
 struct AttnCfg {
   static constexpr int kOver = 0;
+  static constexpr float kOutUnit = kUnbias;                // what the accumulators and partials count
   static constexpr int kD = kD_, kNT = kNT_, kRW = kRW_, kKW = kKW_, kSlots = kSlots_, kCtas = kCtas_;
   static constexpr int kRowsPerWarp = 8 * kNT;
   static constexpr int kRows = kRowsPerWarp * kRW;
@@ -101,14 +104,12 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 // exponentials of its own; a piece's outputs are brought to that reference at its end.  (Up to there
 // the factor 2^(m - m') of a new maximum leaves fp32's range only where the sum so far has no bits in
 // the new one: -126 + 2 * 48 = -30.)
-constexpr int kBias = 15;
 constexpr int kMinExp = -100;
 constexpr float kSameExp = 48.0f;
 static_assert(kSameExp <= kFarExp, "the reference so far is the sum's own");
 __device__ __forceinline__ float v_exponent(int byte) {
   return byte == 255 ? __uint_as_float(0x7FC00000u) : (float)max(byte - 127, kMinExp);
 }
-static_assert(kUnbias == 1.0f / (1 << kBias), "the partials' unit is the weights'");
 
 __device__ __forceinline__ uint32_t lds32(const uint8_t* p) { return *reinterpret_cast<const uint32_t*>(p); }
 
@@ -121,13 +122,19 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
 
 // Adds the exponentials of a tile's scores to two rows' sums whose references stand at `ref` and `ref + 1`: a, b the
 // scores of the halves' keys as they lie (row 0, row 1, row 0, row 1), f their factors (a's two, b's two), e_base V's
-// exponents and what the scores count from, bit 4 b + i of `masked` a score that is not.  (A call, since its code in
-// the tiles' own cost them 2 to 6 % of their time.)
-__device__ __noinline__ float2 far_sums(const float4 a, const float4 b, const float4 f, const float4 e_base, const float2 l,
-                                        const uint32_t masked, float* const ref) {
+// exponents and what the scores count from, bit 4 b + i of `masked` a score that is not.  Returns the sums, where the
+// references stand from what the scores count from, and their changes: the outputs' references go by those, since
+// fp32 holds large scores in steps that V's exponents are lost in.  (A call, since its code in the tiles' own cost
+// them 2 to 6 % of their time.)
+struct FarSums {
+  float l[2], at[2], change[2];
+};
+__device__ __noinline__ FarSums far_sums(const float4 a, const float4 b, const float4 f, const float4 e_base, const float2 l,
+                                         const uint32_t masked, float* const ref) {
   const float s[2][4] = {{a.x, a.y, a.z, a.w}, {b.x, b.y, b.z, b.w}};
   const float fs[2][2] = {{f.x, f.y}, {f.z, f.w}}, base[2] = {e_base.z, e_base.w};
   float sums[2] = {l.x, l.y};
+  FarSums r;
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     float mx = fmaxf(fmaf(fmaxf(s[0][e], s[0][2 + e]), fs[0][e], near_exponent(e_base.x)),
@@ -147,8 +154,11 @@ __device__ __noinline__ float2 far_sums(const float4 a, const float4 b, const fl
       const int mk = q >> 1, at = 2 * (q & 1) + e;
       if (!((masked >> (4 * mk + at)) & 1u)) sums[e] += ex2(fmaf(s[mk][at], fs[mk][e], -less));
     }
+    r.l[e] = sums[e];
+    r.at[e] = less;
+    r.change[e] = top > before ? before - top : 0.0f;
   }
-  return make_float2(sums[0], sums[1]);
+  return r;
 }
 
 template <class C>
@@ -382,7 +392,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
     // This lane's rows: 8 n + 2 t and the next of its warp's; keys of a tile: 16 mk + g and + 8.
     float o[kD / 16][kNT][4];
     float m[kNT][2], l[kNT][2], rf[kNT][2];
-    bool far = false;  // the sums' references are not m (the same for the warp), and stand in s_m
+    bool far = false;  // the sums have references of their own (the same for the warp), in s_m, and m counts from them
     int lim[kNT][2];
 #pragma unroll
     for (int n = 0; n < kNT; ++n) {
@@ -462,6 +472,10 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
 #pragma unroll
             for (int e = 0; e < 2; ++e) s_m[kw * kRows + rw * C::kRowsPerWarp + n * 8 + 2 * t + e] = m[n][e];
         __syncwarp();
+#pragma unroll
+        for (int n = 0; n < kNT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) m[n][e] = m[n][e] == -INFINITY ? -INFINITY : 0.0f;
       }
       if (far) h0.z = h1.z = 0.0f;  // what sums take of the weights
 
@@ -514,7 +528,20 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
             f0[e] = f1[e] = 1.0f;
           }
         }
-        float m_new[2], local[2];
+        float m_new[2], local[2], from0[2] = {base[0], base[1]};  // where m's numbers count from, seen from the scores'
+        if (far) {
+          const FarSums r =
+              far_sums(make_float4(s[0][n][0], s[0][n][1], s[0][n][2], s[0][n][3]),
+                       make_float4(s[1][n][0], s[1][n][1], s[1][n][2], s[1][n][3]), make_float4(f0[0], f0[1], f1[0], f1[1]),
+                       make_float4(h0.y, h1.y, base[0], base[1]), make_float2(l[n][0], l[n][1]), masked,
+                       s_m + kw * kRows + rw * C::kRowsPerWarp + n * 8 + 2 * t);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            l[n][e] = r.l[e];
+            m[n][e] += r.change[e];
+            from0[e] = -r.at[e];
+          }
+        }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float x0 = fmaf(fmaxf(s[0][n][e], s[0][n][2 + e]), f0[e], h0.y);
@@ -524,7 +551,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
           local[e] = mx;
-          m_new[e] = fmaxf(m[n][e], mx + base[e]);
+          m_new[e] = fmaxf(m[n][e], mx + from0[e]);
         }
         if (__any_sync(0xffffffffu, m_new[0] > m[n][0] || m_new[1] > m[n][1])) {
           float alpha[2];
@@ -539,20 +566,13 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[d][n][e] *= alpha[e & 1];
         }
-        if (far) {
-          const float2 sums =
-              far_sums(make_float4(s[0][n][0], s[0][n][1], s[0][n][2], s[0][n][3]),
-                       make_float4(s[1][n][0], s[1][n][1], s[1][n][2], s[1][n][3]), make_float4(f0[0], f0[1], f1[0], f1[1]),
-                       make_float4(h0.y, h1.y, base[0], base[1]), make_float2(l[n][0], l[n][1]), masked,
-                       s_m + kw * kRows + rw * C::kRowsPerWarp + n * 8 + 2 * t);
-          l[n][0] = sums.x;
-          l[n][1] = sums.y;
-        }
         float b0[2], b1[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           // -m + kBias for scores counted from `base`.
-          const float from = base[e] == 0.0f ? m[n][e] : local[e] - ((local[e] + base[e]) - m[n][e]);
+          const float from = far               ? m[n][e] - from0[e]
+                             : base[e] == 0.0f ? m[n][e]
+                                               : local[e] - ((local[e] + base[e]) - m[n][e]);
           const float less = m[n][e] == -INFINITY ? 0.0f : from - (float)kBias;
           b0[e] = h0.y - less;
           b1[e] = h1.y - less;
@@ -689,7 +709,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
         float mx = s_m[r];
 #pragma unroll
         for (int k = 1; k < kKW; ++k) mx = fmaxf(mx, s_m[k * kRows + r]);
-        const float w = mx == -INFINITY ? 1.0f : exp2f(m[n][e] - mx);
+        const float w = mx == -INFINITY ? 1.0f : exp2f(far ? m[n][e] + (s_m[kw * kRows + r] - mx) : m[n][e] - mx);
         float* dst = merge + (size_t)(kw * kRows + r) * C::kPitch + 4 * g;
 #pragma unroll
         for (int dg = 0; dg < kD / 32; ++dg)

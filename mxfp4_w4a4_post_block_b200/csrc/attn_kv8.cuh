@@ -114,9 +114,6 @@ __device__ __forceinline__ Pow2 pow2_of(float e) {
 }
 __device__ __forceinline__ float times(float v, Pow2 p) { return v * p.a * p.b; }
 
-// Outputs in the partials count this (attn_kv8.cu has the weights' bias).
-constexpr float kUnbias = 1.0f / 32768.0f;
-
 // Bit 7 of every byte that is an E4M3 NaN (all of its low seven bits set).
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
   return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
@@ -213,7 +210,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_attn_kv8_join(const AttnArg
       for (int i = 0; i < kPer; ++i) acc[i] = fmaf(weight.a * s_acc[first + w][lane * kPer + i], weight.b, acc[i]);
     }
   }
-  const float inv = sum == 0.0f ? 0.0f : kUnbias / sum;  // a row that sees nothing: zeros
+  const float inv = sum == 0.0f ? 0.0f : C::kOutUnit / sum;  // a row that sees nothing: zeros
 #pragma unroll
   for (int i = 0; i < kPer; i += 2) {
     if (a.out_bf16)

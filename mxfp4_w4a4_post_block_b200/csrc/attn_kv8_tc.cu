@@ -59,6 +59,7 @@ constexpr float kLeastRise = -111.0f;    // what lies below has fewer digits (th
 template <int kLive, int kGroups_, int kSlots_, int kCtas_, int kOver_>
 struct TcCfg {
   static constexpr int kOver = kOver_;
+  static constexpr float kOutUnit = kWeightUnit;  // what the accumulators and partials count
   static constexpr int kD = 128, kRows = kLive, kUnit = kTcTile, kGroups = kGroups_, kSlots = kSlots_, kCtas = kCtas_;
   // Up to 24 rows, the parts of a row are columns of their own, so that an instruction reads its tile of K or V
   // once for all of them.  Above, TMEM has room for two of them: K's instructions take the first two parts
@@ -668,7 +669,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
         }
 
         // The exponent above each row's largest of the warp's keys, and whether a row has outgrown its reference.
-        float held[kHeld], weights[kHeld];
+        float held[kHeld], local[kHeld], weights[kHeld];
         auto largest = [&](float exponent, float* to, float (&of)[kHeld]) {
 #pragma unroll
           for (int r = 0; r < kLive; r += 4) {
@@ -713,7 +714,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
         largest(near_exponent(f.y), mx_of + w4 * kLive, held);
 #pragma unroll
         for (int k = 0; k < kHeld; ++k) {
-          weights[k] = held[k];
+          weights[k] = local[k] = held[k];
           held[k] += base[k];
         }
         const bool far = __any_sync(0xffffffffu, named && fabsf(f.y) > kFarExp);
@@ -781,12 +782,15 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
         for (int k = 0; k < kHeld; ++k) {
           const int r = lane + 32 * k;
           if (r < kLive) {
-            float rise = weights[k] > kNoRef ? fminf(weights[k] + base[k] - ref_of[r], kMostRise) : 0.0f;
+            // (`local` stands at held - reference; all else of the tile goes by its distance from it, since fp32 holds
+            // large scores in steps that V's exponents are lost in)
+            const float at = local[k] > kNoRef ? held[k] - ref_of[r] : 0.0f;
+            float rise = weights[k] > kNoRef ? fminf(at + (weights[k] - local[k]), kMostRise) : 0.0f;
             if (rise < kLeastRise) {
               nb_of[r] += rise - kLeastRise;
               rise = kLeastRise;
             }
-            mx_of[w4 * kLive + r] = base[k] - ref_of[r];
+            mx_of[w4 * kLive + r] = local[k] > kNoRef ? at - local[k] : 0.0f;
             fac_of[r] = ex2(rise - 20.0f);
             uint8_t* sf = s_sfp + buf * kSfAtom + w4;
             if constexpr (C::kStacked) {
@@ -938,9 +942,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
                 make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
           if (a.lse && lane == 0) a.lse[row * a.q_heads + head] = sum == 0.0f ? -INFINITY : kLn2 * (m + log2f(sum));
         } else {
-          constexpr float kUnit = kWeightUnit / kUnbias;  // what the join divides by
-          *reinterpret_cast<float4*>(a.partial + ((size_t)part_slot * kLive + r) * 128 + lane * 4) =
-              make_float4(v.x * kUnit, v.y * kUnit, v.z * kUnit, v.w * kUnit);
+          *reinterpret_cast<float4*>(a.partial + ((size_t)part_slot * kLive + r) * 128 + lane * 4) = v;
           if (lane == 0) {
             float* ml = a.partial + (size_t)2 * a.runs * kLive * 128;
             ml[(size_t)part_slot * kLive + r] = m;
