@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
       if (lane == 0) set_error(a.err, kErrDataTimeout);
       return ok = false;
     };
-    // Tile i, whose K has landed.  kWhole: nothing of it is masked (all but a sequence's last tiles).
+    // Tile i, whose K has landed.  kWhole: nothing of it is masked (all but a sequence's last tiles), and not `far`.
     auto tile = [&](auto whole_tag, const int i, const int key, float4 h0, float4 h1) {
       constexpr bool kWhole = decltype(whole_tag)::value;
       const uint32_t named = kWhole ? 3u : __float_as_uint(h0.w);
@@ -464,20 +464,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
         }
       }
       release(2 * i);
-      if (!far && fmaxf(fabsf(h0.y), fabsf(h1.y)) > kSameExp) {
-        far = true;
-        if (g == 0)
-#pragma unroll
-          for (int n = 0; n < kNT; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) s_m[kw * kRows + rw * C::kRowsPerWarp + n * 8 + 2 * t + e] = m[n][e];
-        __syncwarp();
-#pragma unroll
-        for (int n = 0; n < kNT; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) m[n][e] = m[n][e] == -INFINITY ? -INFINITY : 0.0f;
-      }
-      if (far) h0.z = h1.z = 0.0f;  // what sums take of the weights
+      if (!kWhole && far) h0.z = h1.z = 0.0f;  // what sums take of the weights
 
       // Softmax.  The maximum is taken of the raw scores, whose factor is positive.
       uint32_t pb[2][kNT][2];  // P^T: the second product's operand
@@ -528,8 +515,8 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
             f0[e] = f1[e] = 1.0f;
           }
         }
-        float m_new[2], local[2], from0[2] = {base[0], base[1]};  // where m's numbers count from, seen from the scores'
-        if (far) {
+        float m_new[2], local[2];
+        if (!kWhole && far) {
           const FarSums r =
               far_sums(make_float4(s[0][n][0], s[0][n][1], s[0][n][2], s[0][n][3]),
                        make_float4(s[1][n][0], s[1][n][1], s[1][n][2], s[1][n][3]), make_float4(f0[0], f0[1], f1[0], f1[1]),
@@ -539,7 +526,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
           for (int e = 0; e < 2; ++e) {
             l[n][e] = r.l[e];
             m[n][e] += r.change[e];
-            from0[e] = -r.at[e];
+            base[e] = -r.at[e];  // (m counts from there)
           }
         }
 #pragma unroll
@@ -551,7 +538,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
           local[e] = mx;
-          m_new[e] = fmaxf(m[n][e], mx + from0[e]);
+          m_new[e] = fmaxf(m[n][e], mx + base[e]);
         }
         if (__any_sync(0xffffffffu, m_new[0] > m[n][0] || m_new[1] > m[n][1])) {
           float alpha[2];
@@ -559,7 +546,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
           for (int e = 0; e < 2; ++e) {
             alpha[e] = m_new[e] > m[n][e] ? ex2(m[n][e] - m_new[e]) : 1.0f;
             m[n][e] = m_new[e];
-            if (!far) l[n][e] *= alpha[e];
+            if (kWhole || !far) l[n][e] *= alpha[e];
           }
 #pragma unroll
           for (int d = 0; d < kD / 16; ++d)
@@ -570,9 +557,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           // -m + kBias for scores counted from `base`.
-          const float from = far               ? m[n][e] - from0[e]
-                             : base[e] == 0.0f ? m[n][e]
-                                               : local[e] - ((local[e] + base[e]) - m[n][e]);
+          const float from = base[e] == 0.0f ? m[n][e] : local[e] - ((local[e] + base[e]) - m[n][e]);
           const float less = m[n][e] == -INFINITY ? 0.0f : from - (float)kBias;
           b0[e] = h0.y - less;
           b1[e] = h1.y - less;
@@ -673,7 +658,20 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
       if (!landed()) break;
       const float4 h0 = meta[2 * (i % C::kMetas)], h1 = meta[2 * (i % C::kMetas) + 1];
       const int key = key0 + (i * kKW + kw) * kTile;
-      if (key + kTile <= full_end && __float_as_uint(h0.w) == 3u)
+      if (!far && fmaxf(fabsf(h0.y), fabsf(h1.y)) > kSameExp) {
+        far = true;
+        if (g == 0)
+#pragma unroll
+          for (int n = 0; n < kNT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) s_m[kw * kRows + rw * C::kRowsPerWarp + n * 8 + 2 * t + e] = m[n][e];
+        __syncwarp();
+#pragma unroll
+        for (int n = 0; n < kNT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) m[n][e] = m[n][e] == -INFINITY ? -INFINITY : 0.0f;
+      }
+      if (key + kTile <= full_end && __float_as_uint(h0.w) == 3u && !far)
         tile(std::true_type{}, i, key, h0, h1);
       else
         tile(std::false_type{}, i, key, h0, h1);

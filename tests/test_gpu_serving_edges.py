@@ -407,3 +407,49 @@ def test_w4a16_bf16_outputs_beside_an_outlier(S, x_dtype, fmt):
     tol = each @ np.abs(w).T + (np.abs(xd) * (np.arange(N) != 10)) @ np.abs(w).T * (N / 8 + 24) * 2.0 ** -23 + np.abs(ref) * 2.0 ** -8
     err = np.abs(out.double().cpu().numpy() - ref)
     assert (err <= tol).all(), (err / tol).max()
+
+
+@pytest.mark.parametrize("D,G,tokens", [(64, 3, 0), (64, 24, 0), (128, 5, 0), (256, 16, 0), (128, 5, 2049), (128, 20, 2049),
+                                        (128, 44, 2049)])
+@pytest.mark.parametrize("k_spread", [3.0, 12.0])
+@pytest.mark.parametrize("seed", [1, 2, 3])
+def test_attention_large_scores_beside_page_scales_apart(D, G, tokens, k_spread, seed):
+    """Scores up to 2^40, which fp32 holds in steps that V's exponents are lost in, with V scales anywhere: each row is an
+    average of its tokens' values, finite, and where one token is clearly ahead that token's."""
+    rng = np.random.default_rng(seed)
+    page, lens = 16, [1500, 700, 33, 16, 1501]
+    c = spread_case(70 + seed, 1, G, D, page, lens, lambda p, n: int(rng.choice([1, 40, 100, 127, 160, 200, 240])))
+    c[5] = np.clip(np.round(rng.standard_normal(c[5].shape) * k_spread + 119), 60, 190).astype(np.uint8)
+    c = long_table(c, page, tokens)
+    out, lse = attn_run(*c, 0.1, 1, out_dtype=F32)
+    attn_check(out, None, *c, 0.1, 1)
+    k, v = (R.e4m3_value(a) * R.e8m0_value(s)[..., None, None] for a, s in ((c[4], c[5]), (c[6], c[7])))
+    seen = 0
+    for b, L in enumerate(lens):
+        ids = c[3][b, :(L + page - 1) // page]
+        kk, vv = (a[ids, 0].reshape(-1, D)[:L] for a in (k, v))
+        for h in range(G):
+            s = kk @ c[0].view(-1, G, D)[b, h].double().numpy() * 0.1
+            got = out.view(-1, G, D)[b, h].double().cpu().numpy()
+            assert np.isfinite(got).all() and (np.abs(got) <= np.abs(vv).max(0) * (1 + 2.0 ** -9)).all()
+            order = np.sort(s)
+            if L == 1 or order[-1] - order[-2] > 200 + np.abs(s).max() * 2.0 ** -15:  # e^-200 times 2^113 is nothing beside 2^-126
+                assert np.abs(got - vv[s.argmax()]).max() <= np.abs(vv[s.argmax()]).max() * 2.0 ** -10 + 2.0 ** -126
+                seen += 1
+    assert seen or k_spread < 10
+
+
+@pytest.mark.parametrize("G", [4, 20, 40])
+def test_long_attention_partials_of_the_largest_values(G):
+    """V near fp32's largest (scale 2^120), scores that rise by about 43 from one 128 keys to the next, which is less than a
+    reference's slack, in items cut by run borders: partials stay finite."""
+    page, lens = 32, [2200] * 40
+    c = spread_case(80, 1, G, 128, page, lens, lambda p, n: 247)
+    c[0].abs_()
+    c[4] = c[4] & 0x7F  # keys and queries of one sign, so that scores rise with K's scales
+    for b in range(len(lens)):
+        c[5][c[3][b], 0] = np.where(np.arange(len(c[3][b])) // 4 % 2 == 0, 119, 125).astype(np.uint8)
+    c = long_table(c, page)
+    out, lse = attn_run(*c, 0.028, 1, out_dtype=F32)
+    attn_check(out, None, *c, 0.028, 1)
+    lse_check(lse, *c[:6], 0.028, 1, True)
