@@ -124,12 +124,11 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
 // scores of the halves' keys as they lie (row 0, row 1, row 0, row 1), f their factors (a's two, b's two), e_base V's
 // exponents and what the scores count from, bit 4 b + i of `masked` a score that is not.  Returns the sums, where the
 // references stand from what the scores count from, and their changes: the outputs' references go by those, since
-// fp32 holds large scores in steps that V's exponents are lost in.  (A call, since its code in the tiles' own cost
-// them 2 to 6 % of their time.)
+// fp32 holds large scores in steps that V's exponents are lost in.
 struct FarSums {
   float l[2], at[2], change[2];
 };
-__device__ __noinline__ FarSums far_sums(const float4 a, const float4 b, const float4 f, const float4 e_base, const float2 l,
+__device__ __forceinline__ FarSums far_sums(const float4 a, const float4 b, const float4 f, const float4 e_base, const float2 l,
                                          const uint32_t masked, float* const ref) {
   const float s[2][4] = {{a.x, a.y, a.z, a.w}, {b.x, b.y, b.z, b.w}};
   const float fs[2][2] = {{f.x, f.y}, {f.z, f.w}}, base[2] = {e_base.z, e_base.w};
@@ -425,9 +424,9 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
       if (lane == 0) set_error(a.err, kErrDataTimeout);
       return ok = false;
     };
-    // Tile i, whose K has landed.  kWhole: nothing of it is masked (all but a sequence's last tiles), and not `far`.
-    auto tile = [&](auto whole_tag, const int i, const int key, float4 h0, float4 h1) {
-      constexpr bool kWhole = decltype(whole_tag)::value;
+    // Tile i, whose K has landed.  kWhole: nothing of it is masked (all but a sequence's last tiles); kFar: `far`.
+    auto tile = [&](auto whole_tag, auto far_tag, const int i, const int key, const float4 h0, const float4 h1) {
+      constexpr bool kWhole = decltype(whole_tag)::value, kFar = decltype(far_tag)::value;
       const uint32_t named = kWhole ? 3u : __float_as_uint(h0.w);
 
       // S^T: two 16-key tiles by the warp's rows.
@@ -464,7 +463,6 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
         }
       }
       release(2 * i);
-      if (!kWhole && far) h0.z = h1.z = 0.0f;  // what sums take of the weights
 
       // Softmax.  The maximum is taken of the raw scores, whose factor is positive.
       uint32_t pb[2][kNT][2];  // P^T: the second product's operand
@@ -516,7 +514,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
           }
         }
         float m_new[2], local[2];
-        if (!kWhole && far) {
+        if constexpr (kFar) {
           const FarSums r =
               far_sums(make_float4(s[0][n][0], s[0][n][1], s[0][n][2], s[0][n][3]),
                        make_float4(s[1][n][0], s[1][n][1], s[1][n][2], s[1][n][3]), make_float4(f0[0], f0[1], f1[0], f1[1]),
@@ -546,7 +544,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
           for (int e = 0; e < 2; ++e) {
             alpha[e] = m_new[e] > m[n][e] ? ex2(m[n][e] - m_new[e]) : 1.0f;
             m[n][e] = m_new[e];
-            if (kWhole || !far) l[n][e] *= alpha[e];
+            if (!kFar) l[n][e] *= alpha[e];
           }
 #pragma unroll
           for (int d = 0; d < kD / 16; ++d)
@@ -571,7 +569,7 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
             p[e] = ex2(fmaf(s[mk][n][e], mk == 0 ? f0[e & 1] : f1[e & 1], mk == 0 ? b0[e & 1] : b1[e & 1]));
             if (!kWhole && ((masked >> (4 * mk + e)) & 1u))
               p[e] = 0.0f;  // (a NaN scale is not for this row's sum either)
-            else
+            else if (!kFar)
               l[n][e & 1] = fmaf(p[e], hh.z, l[n][e & 1]);
           }
           if (hh.y == (float)kMinExp) {
@@ -654,27 +652,34 @@ __global__ void __launch_bounds__(C::kThreads, C::kCtas)
       }
       release(2 * i + 1);
     };
-    for (int i = 0; i < my_tiles && ok; ++i) {
+    int i = 0;
+    for (; i < my_tiles && ok; ++i) {
       if (!landed()) break;
       const float4 h0 = meta[2 * (i % C::kMetas)], h1 = meta[2 * (i % C::kMetas) + 1];
+      if (fmaxf(fabsf(h0.y), fabsf(h1.y)) > kSameExp) break;
       const int key = key0 + (i * kKW + kw) * kTile;
-      if (!far && fmaxf(fabsf(h0.y), fabsf(h1.y)) > kSameExp) {
-        far = true;
-        if (g == 0)
-#pragma unroll
-          for (int n = 0; n < kNT; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) s_m[kw * kRows + rw * C::kRowsPerWarp + n * 8 + 2 * t + e] = m[n][e];
-        __syncwarp();
-#pragma unroll
-        for (int n = 0; n < kNT; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) m[n][e] = m[n][e] == -INFINITY ? -INFINITY : 0.0f;
-      }
-      if (key + kTile <= full_end && __float_as_uint(h0.w) == 3u && !far)
-        tile(std::true_type{}, i, key, h0, h1);
+      if (key + kTile <= full_end && __float_as_uint(h0.w) == 3u)
+        tile(std::true_type{}, std::false_type{}, i, key, h0, h1);
       else
-        tile(std::false_type{}, i, key, h0, h1);
+        tile(std::false_type{}, std::false_type{}, i, key, h0, h1);
+    }
+    // From the first tile of far scales on.  (A loop of its own: among the other tiles' code it cost 3 short sequences
+    // 6.2 -> 6.4 us, as a call from there as much.)
+    if (i < my_tiles && ok) {
+      far = true;
+#pragma unroll
+      for (int n = 0; n < kNT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if (g == 0) s_m[kw * kRows + rw * C::kRowsPerWarp + n * 8 + 2 * t + e] = m[n][e];
+          m[n][e] = m[n][e] == -INFINITY ? -INFINITY : 0.0f;
+        }
+      __syncwarp();
+      for (; i < my_tiles && ok; ++i) {
+        if (!landed()) break;
+        const float4 h0 = meta[2 * (i % C::kMetas)], h1 = meta[2 * (i % C::kMetas) + 1];
+        tile(std::false_type{}, std::true_type{}, i, key0 + (i * kKW + kw) * kTile, h0, h1);
+      }
     }
 
     // ---------------------------------------------------------------- join the key groups
