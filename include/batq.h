@@ -702,7 +702,8 @@ BATQ_API batq_status batq_attn_kv8_workspace_size(int max_q_len, int q_heads, in
  * dims 64 and 256, and 128 with max_pages * page_size up to 2048: queries are
  * rounded to f16 after an exact normalisation (bf16 queries lose nothing down
  * to 2^-28 of the row's largest), the products of probability and V scale to
- * f16, and to 2^-40 of the row's largest.  Head dim 128 with longer tables:
+ * f16, and to 2^-40 of the row's largest (or of 2^-100).  Head dim 128 with
+ * longer tables:
  * bf16 queries lose nothing down to 2^-13 of the largest of their 32 head dims,
  * fp32 queries keep 12 bits, and those products are rounded to 2^-20 of the
  * largest among their 32 tokens (2^-60 of the row's largest).  The scales of a

@@ -32,7 +32,7 @@
 // arithmetic are about 820 of them per 32 keys and 8 rows, at half of the issue slots; so head dim 128 with
 // long page tables has the kernel in attn_kv8_tc.cu.  Measured: 16 sequences of up to 16000 tokens, 4 heads of
 // 8 queries: 33 us at head dim 64 (2.1 TB/s), 67 us at 256 (4.2 TB/s); 3 sequences of 100 tokens 6 us, the
-// launch and one tile's way through it.  More rows cost more softmax: five queries each 75 and 127 us.
+// launch and one tile's way through it.  More rows cost more softmax: five queries each 74 and 130 us.
 #include <cstdint>
 #include <type_traits>
 
