@@ -270,7 +270,7 @@ def test_waiting_calls_let_other_threads_run():
     torch.cuda.synchronize()
     ok()
     assert longest > 0.3, "no call waited"
-    assert gaps[0] < 0.1, (gaps[0], longest, time.perf_counter() - t0)
+    assert gaps[0] < longest / 2, (gaps[0], longest, time.perf_counter() - t0)
 
 
 FIRST_CALLS = """
@@ -373,16 +373,17 @@ def test_attention_more_queries_allowed_than_there_are(D, G, tokens):
     d = [R.cuda(a) for a in c[2:]]
     q, out = c[0].cuda(), torch.empty(7, 2 * G * D, dtype=BF, device="cuda")
     ws = torch.empty(BQ.batq_attn_kv8_workspace_size(300000, 2 * G, 2, D), dtype=torch.uint8, device="cuda")
-    times = []
-    for m in (1, 300000):
-        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
-        for i in range(60):
-            if i == 10:
-                a.record()
-            BQ.batq_attn_kv8(q, None, *d, 0.1, m, ws, out)
-        b.record()
-        torch.cuda.synchronize()
-        times.append(a.elapsed_time(b))
+    times = [1e9, 1e9]
+    for _ in range(5):
+        for k, m in enumerate((1, 300000)):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            for i in range(60):
+                if i == 10:
+                    a.record()
+                BQ.batq_attn_kv8(q, None, *d, 0.1, m, ws, out)
+            b.record()
+            torch.cuda.synchronize()
+            times[k] = min(times[k], a.elapsed_time(b))
     assert times[1] < 2 * times[0] + 0.2, times
 
 
